@@ -32,6 +32,9 @@ AFD_ERR_STOPPED = -9
 AFD_MAILBOX_PINNED = 1
 AFD_DT_BF16 = 0
 AFD_DT_FP8_E4M3 = 1
+AFD_DT_F32 = 2
+AFD_SCORE_SOFTMAX = 0
+AFD_SCORE_SIGMOID = 1
 AFD_FFN_NUM_STAGES = 9
 STAGE_NAMES = ("router_logits", "router_topk", "dispatch_order", "gather_rows", "gemm_schedule",
                "gemm_gate_up", "quantize_act", "gemm_down", "combine")
@@ -50,6 +53,23 @@ class afd_ffn_weights(ctypes.Structure):
                 ("w13_scale", ctypes.c_void_p), ("w2_scale", ctypes.c_void_p)]
 
 
+class afd_ffn_routing(ctypes.Structure):
+    _fields_ = [("score", ctypes.c_int32), ("n_groups", ctypes.c_int32), ("topk_groups", ctypes.c_int32),
+                ("group_best", ctypes.c_int32), ("renormalise", ctypes.c_int32), ("weight_scale", ctypes.c_float)]
+
+
+class afd_ffn_w4(ctypes.Structure):
+    _fields_ = [("codes", ctypes.c_void_p), ("scale", ctypes.c_void_p), ("zero", ctypes.c_void_p),
+                ("N", ctypes.c_int32), ("K", ctypes.c_int32), ("group", ctypes.c_int32),
+                ("scale_dtype", ctypes.c_int32)]
+
+
+class afd_ffn_norm_cfg(ctypes.Structure):
+    _fields_ = [("T", ctypes.c_int32), ("H", ctypes.c_int32), ("residual_dtype", ctypes.c_int32),
+                ("gamma_dtype", ctypes.c_int32), ("x_stride", ctypes.c_int64), ("residual_stride", ctypes.c_int64),
+                ("sum_stride", ctypes.c_int64), ("out_stride", ctypes.c_int64), ("eps", ctypes.c_float)]
+
+
 class afd_ffn_service_stats(ctypes.Structure):
     _fields_ = [("served", ctypes.c_int64), ("status", ctypes.c_int32), ("device_status", ctypes.c_int32),
                 ("last_cuda_error", ctypes.c_int32), ("reserved", ctypes.c_int32)]
@@ -58,6 +78,7 @@ class afd_ffn_service_stats(ctypes.Structure):
 _P = ctypes.c_void_p
 _I = ctypes.c_int32
 _L = ctypes.c_int64
+_W4 = ctypes.POINTER(afd_ffn_w4)
 _SIGNATURES = {
     "afd_ffn_create": (ctypes.c_int, [ctypes.POINTER(afd_ffn_cfg), ctypes.POINTER(afd_ffn_weights),
                                       ctypes.POINTER(ctypes.c_void_p)]),
@@ -84,6 +105,12 @@ _SIGNATURES = {
     "afd_ffn_dispatch_rows_fp8": (ctypes.c_int, [_P, _P, _I, _I, _I, _I, _I, _P, _P, _P, _P, _P, _P, _P, _P]),
     "afd_ffn_expert_rows_fp8": (ctypes.c_int, [_P, _P, _P, _P, _I, _P, _P]),
     "afd_ffn_combine_rows_bf16": (ctypes.c_int, [_P, _P, _P, _P, _I, _I, _I, _P, _P]),
+    "afd_ffn_select_experts": (ctypes.c_int, [_P, _I, _L, _P, _I, _I, _I, ctypes.POINTER(afd_ffn_routing), _P, _P, _P]),
+    "afd_ffn_set_routing": (ctypes.c_int, [_P, ctypes.POINTER(afd_ffn_routing), _P]),
+    "afd_ffn_w4_rows": (ctypes.c_int, [_W4, _I, _P, _P, _I, _P, _I, _P]),
+    "afd_ffn_w4_expert_rows": (ctypes.c_int, [_W4, _W4, _I, _P, _P, _I, _P, _I, _P, _P]),
+    "afd_ffn_w4_scratch_bytes": (ctypes.c_int64, [_I, _I]),
+    "afd_ffn_add_rmsnorm": (ctypes.c_int, [ctypes.POINTER(afd_ffn_norm_cfg), _P, _P, _P, _P, _P, _P, _P, _P]),
     "afd_ffn_rows_error": (ctypes.c_int, []),
     "afd_ffn_get_info": (ctypes.c_int, [_P, ctypes.POINTER(afd_ffn_cfg), ctypes.POINTER(ctypes.c_int32)]),
     "afd_ffn_check_bounded_wait": (ctypes.c_int, [ctypes.POINTER(ctypes.c_int64)]),
@@ -281,6 +308,76 @@ def afd_ffn_combine_rows(Y, Ys, topk_w, pos, T, k, H, out, stream=None) -> int:
                                      _stream(stream))
 
 
+# expert selection, 4-bit experts, residual addition and norm (declarations in include/afd_ffn.h)
+def _dtype(x):
+    """AFD_DT_* of a tensor."""
+    name = str(x.dtype)
+    return {"torch.bfloat16": AFD_DT_BF16, "torch.float32": AFD_DT_F32}.get(name, -1)
+
+
+def _ref(struct):
+    return ctypes.byref(struct) if struct is not None else None
+
+
+def afd_ffn_select_experts(logits, choice_bias, T, E, k, routing, topk_idx, topk_w, logits_dtype=None,
+                           logits_stride=None, stream=None) -> int:
+    """logits_dtype and logits_stride default to the tensor's own."""
+    if logits_dtype is None:
+        logits_dtype = _dtype(logits)
+    if logits_stride is None:
+        logits_stride = logits.stride(0) if T > 1 else 0
+    return _lib.afd_ffn_select_experts(_ptr(logits), logits_dtype, logits_stride, _ptr(choice_bias), T, E, k,
+                                       _ref(routing), _ptr(topk_idx), _ptr(topk_w), _stream(stream))
+
+
+def afd_ffn_set_routing(h, routing, choice_bias=None) -> int:
+    """choice_bias is borrowed: keep it alive until the next afd_ffn_set_routing or destroy."""
+    return _lib.afd_ffn_set_routing(h, _ref(routing), _ptr(choice_bias))
+
+
+def w4_weights(codes, scale, zero=None, group=None) -> afd_ffn_w4:
+    """The description of 4-bit weights held as device tensors: codes uint8 [E, N, K/2] (or [N, K/2]
+    for one matrix), scale [..., N, K/group] bf16 or fp32, zero uint8 of the same shape or None.
+    group defaults to what the shapes say.  The tensors stay referenced by the result."""
+    N, K = codes.shape[-2], 2 * codes.shape[-1]
+    if group is None:
+        group = K // scale.shape[-1]
+    for t in (scale, zero):
+        if t is not None and (tuple(t.shape) != tuple(codes.shape[:-1]) + (K // group,) or not t.is_contiguous()):
+            raise ValueError(f"scale and zero are contiguous [..., N, K/group]: got {tuple(t.shape)}")
+    if str(codes.dtype) != "torch.uint8" or not codes.is_contiguous():
+        raise ValueError("codes are contiguous uint8 [..., N, K/2]")
+    if zero is not None and str(zero.dtype) != "torch.uint8":
+        raise ValueError("zero is uint8")
+    w = afd_ffn_w4(_ptr(codes), _ptr(scale), _ptr(zero), N, K, group, _dtype(scale))
+    w._keep = (codes, scale, zero)
+    return w
+
+
+def afd_ffn_w4_rows(w, E, x, counts, n_rows, y, y_dtype=None, stream=None) -> int:
+    """y_dtype defaults to the tensor's own."""
+    if y_dtype is None:
+        y_dtype = _dtype(y)
+    return _lib.afd_ffn_w4_rows(_ref(w), E, _ptr(x), _ptr(counts), n_rows, _ptr(y), y_dtype, _stream(stream))
+
+
+def afd_ffn_w4_expert_rows(w13, w2, E, rows, counts, n_rows, Y, scratch, y_dtype=None, stream=None) -> int:
+    """y_dtype defaults to the tensor's own; scratch: afd_ffn_w4_scratch_bytes(n_rows, I) bytes."""
+    if y_dtype is None:
+        y_dtype = _dtype(Y)
+    return _lib.afd_ffn_w4_expert_rows(_ref(w13), _ref(w2), E, _ptr(rows), _ptr(counts), n_rows, _ptr(Y), y_dtype,
+                                       _ptr(scratch), _stream(stream))
+
+
+def afd_ffn_w4_scratch_bytes(n_rows, I) -> int:
+    return _lib.afd_ffn_w4_scratch_bytes(n_rows, I)
+
+
+def afd_ffn_add_rmsnorm(cfg, x, residual, gamma, sum, out, codes=None, row_scale=None, stream=None) -> int:
+    return _lib.afd_ffn_add_rmsnorm(_ref(cfg), _ptr(x), _ptr(residual), _ptr(gamma), _ptr(sum), _ptr(out), _ptr(codes),
+                                    _ptr(row_scale), _stream(stream))
+
+
 def afd_ffn_rows_error() -> int:
     return _lib.afd_ffn_rows_error()
 
@@ -409,6 +506,10 @@ class AfdFfn:
     def route(self, hidden, T, topk_idx, topk_w, stream=None):
         self._check(afd_ffn_route(self.h, hidden, T, topk_idx, topk_w, stream), "afd_ffn_route")
 
+    def set_routing(self, routing, choice_bias=None):
+        self._check(afd_ffn_set_routing(self.h, routing, choice_bias), "afd_ffn_set_routing")
+        self._choice_bias = choice_bias
+
     def permute(self, hidden, topk_idx, T, counts, offsets, pos, src, stream=None):
         self._check(afd_ffn_permute(self.h, hidden, topk_idx, T, counts, offsets, pos, src, stream),
                     "afd_ffn_permute")
@@ -441,4 +542,4 @@ class AfdFfn:
 
 
 __all__ = [n for n in list(globals()) if n.startswith(("afd_ffn", "AFD_", "Afd"))] + [
-    "declared_functions", "LIB_PATH", "STAGE_NAMES"]
+    "declared_functions", "w4_weights", "LIB_PATH", "STAGE_NAMES"]

@@ -20,7 +20,9 @@
 #include "combine.cuh"
 #include "dispatch.cuh"
 #include "gemm.cuh"
+#include "internal.h"
 #include "router.cuh"
+#include "select.cuh"
 
 using namespace afd;
 
@@ -100,6 +102,9 @@ struct afd_ffn_handle {
   float f16_bound = 0.f;     // 2 C / 32768 (w13_norm_bound_kernel): the f16 act row scales' input
   CUtensorMap tm_w2h, tm_act16;
   CUtensorMap tm_xp[2], tm_act[2];  // token rows for the [narrow, wide] shapes (box heights differ)
+  bool routed = false;         // afd_ffn_set_routing: the routing below instead of softmax top-k
+  afd_ffn_routing routing{};
+  const float* choice_bias = nullptr;
   cudaStream_t last_stream = nullptr;
   int last_cuda_error = 0;
   cudaEvent_t events[AFD_FFN_NUM_STAGES + 1];
@@ -436,6 +441,24 @@ void record(afd_ffn_handle* h, int stage, cudaStream_t s) {
   if (h->n_events > stage && h->events[stage]) cudaEventRecord(h->events[stage], s);
 }
 
+SelectArgs select_args(const void* logits, long long ld, int nsplit, const float* logit_bias, const float* choice_bias,
+                       int T, int E, int k, const afd_ffn_routing& r, int32_t* idx, float* w) {
+  return SelectArgs{logits, logit_bias, choice_bias, idx, w, ld, nsplit, T, E, k, r.score == AFD_SCORE_SIGMOID,
+                    r.n_groups, r.topk_groups, r.group_best, r.renormalise, r.weight_scale};
+}
+
+int check_routing(const afd_ffn_routing* r, int E, int k) {
+  if (r->score != AFD_SCORE_SOFTMAX && r->score != AFD_SCORE_SIGMOID) return AFD_ERR_INVALID_ARG;
+  if (r->n_groups < 1 || r->n_groups > E || E % r->n_groups != 0) return AFD_ERR_INVALID_ARG;
+  if (r->topk_groups < 1 || r->topk_groups > r->n_groups || r->topk_groups * (E / r->n_groups) < k)
+    return AFD_ERR_INVALID_ARG;
+  if (r->group_best != 1 && r->group_best != 2) return AFD_ERR_INVALID_ARG;
+  if (r->renormalise != 0 && r->renormalise != 1) return AFD_ERR_INVALID_ARG;
+  if (!(r->weight_scale > 0.f) || !(r->weight_scale <= 3.4e38f)) return AFD_ERR_INVALID_ARG;
+  if (r->n_groups > 32) return AFD_ERR_UNSUPPORTED;
+  return AFD_OK;
+}
+
 // ------------------------------------------------------------------ stages
 // Router on the tensor cores (grouped GEMM, MODE 2): logits [T][E] fp32 into h->part, then the
 // warp-per-token top-k.  The hidden states' TMA descriptor is encoded per call (host only).
@@ -471,7 +494,10 @@ int run_route(afd_ffn_handle* h, const void* hidden, int T, int32_t* idx, float*
   record(h, 1, s);
   // selection and gate weights from the summed partial logits, a warp per token
   const float* bias = c.has_router_bias ? h->w.router_bias : nullptr;
-  launch_router_topk(h->part, ksplit, bias, T, c.E, c.k, idx, w, s);
+  if (h->routed)
+    launch_select_experts<float>(select_args(h->part, c.E, ksplit, bias, h->choice_bias, T, c.E, c.k, h->routing, idx, w), s);
+  else
+    launch_router_topk(h->part, ksplit, bias, T, c.E, c.k, idx, w, s);
   AFD_CUDA(h, cudaGetLastError());
   return AFD_OK;
 }
@@ -935,6 +961,18 @@ int afd_ffn_route(afd_ffn_handle* h, const void* hidden, int32_t T, int32_t* top
   return run_route(h, hidden, T, topk_idx, topk_w, s);
 }
 
+int afd_ffn_set_routing(afd_ffn_handle* h, const afd_ffn_routing* routing, const float* choice_bias) {
+  if (!h || (!routing && choice_bias) || (reinterpret_cast<uintptr_t>(choice_bias) & 3u)) return AFD_ERR_INVALID_ARG;
+  if (routing) {
+    const int st = check_routing(routing, h->cfg.E, h->cfg.k);
+    if (st != AFD_OK) return st;
+    h->routing = *routing;
+  }
+  h->choice_bias = choice_bias;
+  h->routed = routing != nullptr;
+  return AFD_OK;
+}
+
 int afd_ffn_permute(afd_ffn_handle* h, const void* hidden, const int32_t* topk_idx, int32_t T, int32_t* counts,
                     int32_t* offsets, int32_t* pos, int32_t* src, void* stream) {
   if (!h) return AFD_ERR_INVALID_ARG;
@@ -1137,6 +1175,32 @@ extern "C" int afd_ffn_route_static(const void* hidden, const float* router_w, c
   return AFD_OK;
 }
 
+extern "C" int afd_ffn_select_experts(const void* logits, int32_t logits_dtype, int64_t logits_stride,
+                                      const float* choice_bias, int32_t T, int32_t E, int32_t k,
+                                      const afd_ffn_routing* routing, int32_t* topk_idx, float* topk_w, void* stream) {
+  if (!routing || T < 0 || E < 1 || k < 1 || k > E) return AFD_ERR_INVALID_ARG;
+  if (logits_dtype != AFD_DT_BF16 && logits_dtype != AFD_DT_F32) return AFD_ERR_INVALID_ARG;
+  if (E > kMaxExperts || k > 32) return AFD_ERR_UNSUPPORTED;
+  const int st = check_routing(routing, E, k);
+  if (st != AFD_OK) return st;
+  if (logits_stride == 0) logits_stride = E;
+  if (logits_stride < E) return AFD_ERR_INVALID_ARG;
+  if (T == 0) return AFD_OK;
+  const uintptr_t mis = reinterpret_cast<uintptr_t>(logits) & (logits_dtype == AFD_DT_F32 ? 3u : 1u);
+  const uintptr_t mis4 = (reinterpret_cast<uintptr_t>(choice_bias) | reinterpret_cast<uintptr_t>(topk_idx) |
+                          reinterpret_cast<uintptr_t>(topk_w)) & 3u;
+  if (!logits || !topk_idx || !topk_w || mis || mis4) return AFD_ERR_INVALID_ARG;
+  const SelectArgs a = select_args(logits, logits_stride, 1, nullptr, choice_bias, T, E, k, *routing, topk_idx, topk_w);
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (logits_dtype == AFD_DT_F32)
+    launch_select_experts<float>(a, s);
+  else
+    launch_select_experts<__nv_bfloat16>(a, s);
+  const cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess) return cuda_fail(nullptr, e);
+  return AFD_OK;
+}
+
 // ---------------------------------------------------------------------- expert parallelism
 // Building blocks of an expert-parallel layer whose exchange runs outside the library (the
 // dispatch/combine all-to-all of A/F 分离, section 机制): dispatch order and rows without a
@@ -1150,7 +1214,11 @@ namespace {
 std::mutex g_rows_err_mu;
 int* g_rows_err_dev[kMaxDevices] = {};
 
-int rows_err_word(int** out) {
+}  // namespace
+
+int afd::rows_cuda_fail(cudaError_t e) { return cuda_fail(nullptr, e); }
+
+int afd::rows_err_word(int** out) {
   int dev = -1;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return cuda_fail(nullptr, e);
@@ -1165,7 +1233,6 @@ int rows_err_word(int** out) {
   *out = g_rows_err_dev[dev];
   return AFD_OK;
 }
-}  // namespace
 
 extern "C" int afd_ffn_dispatch_rows(const void* hidden, const int32_t* topk_idx, int32_t T, int32_t k, int32_t E,
                                      int32_t H, int32_t* counts, int32_t* offsets, int32_t* pos, int32_t* src,

@@ -1,0 +1,227 @@
+// norm.cu -- residual addition and root-mean-square norm in front of the FFN, with bf16 rows
+// for the router and the bf16 experts and e4m3 rows with one scale each for the W8A8 ones.
+//
+//   s = x + residual (fp32)      sum = s in the residual's type
+//   y = s * (mean(s^2) + eps)^(-1/2) * gamma (fp32, from s before its rounding)
+//   out = bf16(y)      row_scale = max |y| / 448 (1 for a zero row)      codes = e4m3(y / row_scale)
+//
+// Bound by HBM: every byte is read and written once.  One CTA holds a row in registers between
+// the loads and the stores; its one reduction carries both sum(s^2) and max |s gamma|, since
+// max |y| is the latter times the row's factor.
+#include <cuda_bf16.h>
+#include <cuda_fp8.h>
+#include <cuda_runtime.h>
+
+#include "afd_ffn.h"
+#include "common.cuh"
+#include "internal.h"
+
+namespace afd {
+namespace {
+
+constexpr int kNormMaxH = 32768;
+
+struct NormArgs {
+  const void *x, *residual, *gamma;
+  void *sum, *out;
+  uint8_t* codes;
+  float* row_scale;
+  long long ldx, ldr, lds, ldo;
+  int H;
+  float eps;
+};
+
+// V elements from p (V = 8: 16-byte aligned)
+template <int V>
+__device__ __forceinline__ void load_row(const __nv_bfloat16* p, float (&f)[V]) {
+  if constexpr (V == 8) {
+    const uint4 u = *reinterpret_cast<const uint4*>(p);
+    const __nv_bfloat162* b = reinterpret_cast<const __nv_bfloat162*>(&u);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float2 g = __bfloat1622float2(b[i]);
+      f[2 * i] = g.x;
+      f[2 * i + 1] = g.y;
+    }
+  } else {
+    f[0] = __bfloat162float(*p);
+  }
+}
+template <int V>
+__device__ __forceinline__ void load_row(const float* p, float (&f)[V]) {
+  if constexpr (V == 8) {
+    const float4 a = reinterpret_cast<const float4*>(p)[0], b = reinterpret_cast<const float4*>(p)[1];
+    f[0] = a.x; f[1] = a.y; f[2] = a.z; f[3] = a.w;
+    f[4] = b.x; f[5] = b.y; f[6] = b.z; f[7] = b.w;
+  } else {
+    f[0] = *p;
+  }
+}
+template <int V>
+__device__ __forceinline__ void store_row(__nv_bfloat16* p, const float (&f)[V]) {
+  if constexpr (V == 8) {
+    uint4 u;
+    __nv_bfloat162* b = reinterpret_cast<__nv_bfloat162*>(&u);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) b[i] = __floats2bfloat162_rn(f[2 * i], f[2 * i + 1]);
+    *reinterpret_cast<uint4*>(p) = u;
+  } else {
+    *p = __float2bfloat16_rn(f[0]);
+  }
+}
+template <int V>
+__device__ __forceinline__ void store_row(float* p, const float (&f)[V]) {
+  if constexpr (V == 8) {
+    reinterpret_cast<float4*>(p)[0] = make_float4(f[0], f[1], f[2], f[3]);
+    reinterpret_cast<float4*>(p)[1] = make_float4(f[4], f[5], f[6], f[7]);
+  } else {
+    *p = f[0];
+  }
+}
+
+// One CTA per row; thread i takes the pieces of V elements i, i + blockDim, ... (N at most).
+template <int V, int N, typename RT, typename GT>
+__global__ void __launch_bounds__(1024)
+add_rmsnorm_kernel(const NormArgs a) {
+  __shared__ float red[2][32];
+  const long long t = blockIdx.x;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const __nv_bfloat16* x = static_cast<const __nv_bfloat16*>(a.x) + t * a.ldx;
+  const RT* r = static_cast<const RT*>(a.residual) + t * a.ldr;
+  const GT* g = static_cast<const GT*>(a.gamma);
+  const int pieces = a.H / V;
+  float s[N][V];
+  float ss = 0.f, top = 0.f;
+#pragma unroll
+  for (int n = 0; n < N; ++n) {
+    const int p = tid + n * blockDim.x;
+    if (p < pieces) {
+      load_row<V>(x + static_cast<size_t>(p) * V, s[n]);
+      if (a.residual) {
+        float rv[V];
+        load_row<V>(r + static_cast<size_t>(p) * V, rv);
+#pragma unroll
+        for (int i = 0; i < V; ++i) s[n][i] += rv[i];
+      }
+    }
+  }
+#pragma unroll
+  for (int n = 0; n < N; ++n) {
+    const int p = tid + n * blockDim.x;
+    if (p < pieces) {
+      float gv[V];
+      load_row<V>(g + static_cast<size_t>(p) * V, gv);
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        ss = fmaf(s[n][i], s[n][i], ss);
+        top = fmaxf(top, fabsf(s[n][i] * gv[i]));
+      }
+      if (a.sum) store_row<V>(static_cast<RT*>(a.sum) + t * a.lds + static_cast<size_t>(p) * V, s[n]);
+    }
+  }
+  ss = warp_sum(ss);
+  top = warp_max(top);
+  if (lane == 0) {
+    red[0][warp] = ss;
+    red[1][warp] = top;
+  }
+  __syncthreads();
+  const int warps = blockDim.x >> 5;
+  ss = warp_sum(lane < warps ? red[0][lane] : 0.f);  // every warp: the same order, the same sum
+  top = warp_max(lane < warps ? red[1][lane] : 0.f);
+  const float factor = __frsqrt_rn(ss / static_cast<float>(a.H) + a.eps);
+  const float amax = top * factor;
+  const float scale = amax > 0.f ? __fdiv_rn(amax, kE4m3Max) : 1.0f;
+#pragma unroll
+  for (int n = 0; n < N; ++n) {
+    const int p = tid + n * blockDim.x;
+    if (p < pieces) {
+      float y[V];
+      load_row<V>(g + static_cast<size_t>(p) * V, y);
+#pragma unroll
+      for (int i = 0; i < V; ++i) y[i] = s[n][i] * factor * y[i];
+      if (a.out) store_row<V>(static_cast<__nv_bfloat16*>(a.out) + t * a.ldo + static_cast<size_t>(p) * V, y);
+      if (a.codes) {
+        uint8_t* c = a.codes + t * a.H + static_cast<size_t>(p) * V;
+        if constexpr (V == 8) {
+          uint32_t q[2];
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            const float* v = y + 4 * i;
+            const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(__fdiv_rn(v[0], scale), __fdiv_rn(v[1], scale)),
+                                                         __NV_SATFINITE, __NV_E4M3);
+            const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(__fdiv_rn(v[2], scale), __fdiv_rn(v[3], scale)),
+                                                         __NV_SATFINITE, __NV_E4M3);
+            q[i] = lo | (hi << 16);
+          }
+          *reinterpret_cast<uint2*>(c) = make_uint2(q[0], q[1]);
+        } else {
+          *c = __nv_cvt_float_to_fp8(__fdiv_rn(y[0], scale), __NV_SATFINITE, __NV_E4M3);
+        }
+      }
+    }
+  }
+  if (a.codes && tid == 0) a.row_scale[t] = scale;
+}
+
+template <int V, typename RT, typename GT>
+void launch_norm(const NormArgs& a, int T, cudaStream_t s) {
+  const int pieces = a.H / V;
+  const int threads = min(1024, (pieces + 31) / 32 * 32);
+  const int n = (pieces + threads - 1) / threads;
+  if (n <= 1)
+    add_rmsnorm_kernel<V, 1, RT, GT><<<T, threads, 0, s>>>(a);
+  else if (n <= 4)
+    add_rmsnorm_kernel<V, 4, RT, GT><<<T, threads, 0, s>>>(a);
+  else if constexpr (V == 1)
+    add_rmsnorm_kernel<V, 32, RT, GT><<<T, threads, 0, s>>>(a);
+}
+
+template <int V>
+void launch_norm_types(const NormArgs& a, const afd_ffn_norm_cfg& c, cudaStream_t s) {
+  const bool rf = c.residual_dtype == AFD_DT_F32, gf = c.gamma_dtype == AFD_DT_F32;
+  if (rf && gf) launch_norm<V, float, float>(a, c.T, s);
+  else if (rf) launch_norm<V, float, __nv_bfloat16>(a, c.T, s);
+  else if (gf) launch_norm<V, __nv_bfloat16, float>(a, c.T, s);
+  else launch_norm<V, __nv_bfloat16, __nv_bfloat16>(a, c.T, s);
+}
+
+bool elem_dtype(int32_t d) { return d == AFD_DT_BF16 || d == AFD_DT_F32; }
+bool aligned(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
+
+}  // namespace
+}  // namespace afd
+
+using namespace afd;
+
+extern "C" int afd_ffn_add_rmsnorm(const afd_ffn_norm_cfg* cfg, const void* x, const void* residual,
+                                   const void* gamma, void* sum, void* out, void* codes, float* row_scale,
+                                   void* stream) {
+  if (!cfg) return AFD_ERR_INVALID_ARG;
+  const afd_ffn_norm_cfg& c = *cfg;
+  if (c.T < 0 || c.H < 1 || !elem_dtype(c.residual_dtype) || !elem_dtype(c.gamma_dtype)) return AFD_ERR_INVALID_ARG;
+  if (!(c.eps >= 0.f) || !(c.eps <= 3.4e38f)) return AFD_ERR_INVALID_ARG;
+  if (c.H > kNormMaxH) return AFD_ERR_UNSUPPORTED;
+  NormArgs a{x, residual, gamma, sum, out, static_cast<uint8_t*>(codes), row_scale, c.x_stride, c.residual_stride,
+             c.sum_stride, c.out_stride, c.H, c.eps};
+  for (long long* ld : {&a.ldx, &a.ldr, &a.lds, &a.ldo}) {
+    if (*ld == 0) *ld = c.H;
+    if (*ld < c.H) return AFD_ERR_INVALID_ARG;
+  }
+  if (c.T == 0) return AFD_OK;
+  if (!x || !gamma || (sum && !residual) || (!out && !codes) || (!codes != !row_scale)) return AFD_ERR_INVALID_ARG;
+  const uintptr_t rsize = c.residual_dtype == AFD_DT_F32 ? 4 : 2, gsize = c.gamma_dtype == AFD_DT_F32 ? 4 : 2;
+  if (!aligned(x, 2) || !aligned(residual, rsize) || !aligned(sum, rsize) || !aligned(gamma, gsize) ||
+      !aligned(out, 2) || !aligned(row_scale, 4))
+    return AFD_ERR_INVALID_ARG;
+  // 16-byte pieces where every row of every tensor starts on a 16-byte boundary
+  const uintptr_t rper = 16 / rsize;
+  const bool wide = c.H % 8 == 0 && aligned(x, 16) && a.ldx % 8 == 0 && aligned(gamma, 16) &&
+                    (!residual || (aligned(residual, 16) && a.ldr % rper == 0)) &&
+                    (!sum || (aligned(sum, 16) && a.lds % rper == 0)) &&
+                    (!out || (aligned(out, 16) && a.ldo % 8 == 0)) && (!codes || aligned(codes, 8));
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (wide) launch_norm_types<8>(a, c, s); else launch_norm_types<1>(a, c, s);
+  const cudaError_t e = cudaGetLastError();
+  return e == cudaSuccess ? AFD_OK : rows_cuda_fail(e);
+}

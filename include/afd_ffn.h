@@ -58,7 +58,7 @@ extern "C" {
 #define AFD_ERR_STOPPED        (-9)  /* the FFN service stopped before it served the slot       */
 
 /* ---- configuration ---------------------------------------------------------------- */
-typedef enum { AFD_DT_BF16 = 0, AFD_DT_FP8_E4M3 = 1 } afd_dtype;
+typedef enum { AFD_DT_BF16 = 0, AFD_DT_FP8_E4M3 = 1, AFD_DT_F32 = 2 } afd_dtype;
 
 typedef struct {
     int32_t T_max;           /* largest micro-batch any call will pass, >= 1                  */
@@ -114,6 +114,46 @@ void afd_ffn_destroy(afd_ffn_handle *h);
  * (softmax over the selected logits).  0 <= T <= T_max. */
 int afd_ffn_route(afd_ffn_handle *h, const void *hidden, int32_t T,
                   int32_t *topk_idx, float *topk_w, void *stream);
+
+/* How experts are selected and weighted, where the softmax top-k of afd_ffn_route is not what
+ * the model was trained with.  From a token's logits l [E]:
+ *   score    s_e = 1 / (1 + e^-l_e)  or  e^l_e / sum_f e^l_f
+ *   choice   c_e = s_e + choice_bias[e] (the bias steers the selection, not the weights)
+ *   groups   E / n_groups consecutive experts each; a group is worth the sum of its group_best
+ *            largest c; the topk_groups best groups stay (ties: the lower group)
+ *   idx      the k largest c of the groups that stay, descending, ties to the lower expert
+ *   w_j      s of idx[j], divided by the sum over j when renormalise, times weight_scale
+ * Without a bias scores are compared by their logits, whose order they have; choices with a bias
+ * and sums of two are compared as evaluated in 64 bits.  An expert whose logit is -inf or NaN, or whose c is -inf or
+ * NaN, is out of service: it is never selected, and a NaN logit has no share in the softmax.  A
+ * logit of +inf counts as the largest float.  A group with fewer than group_best experts in
+ * service is worth what it has; one with none never stays.  Where fewer than k experts are left,
+ * the slots behind them hold idx -1 and w 0 (the dispatch skips them and sets the error word). */
+typedef enum { AFD_SCORE_SOFTMAX = 0, AFD_SCORE_SIGMOID = 1 } afd_score;
+typedef struct {
+    int32_t score;           /* afd_score                                                     */
+    int32_t n_groups;        /* 1..32, divides E; 1 = no groups                               */
+    int32_t topk_groups;     /* 1..n_groups, with topk_groups * E / n_groups >= k             */
+    int32_t group_best;      /* 1 or 2 (of no effect when topk_groups == n_groups)            */
+    int32_t renormalise;     /* 0 or 1                                                        */
+    float   weight_scale;    /* finite, > 0                                                   */
+} afd_ffn_routing;
+
+/* Select and weigh experts from router logits that the caller has: logits [T][E] bf16 or fp32
+ * (logits_dtype AFD_DT_BF16 / AFD_DT_F32), logits_stride elements from token to token (0 = E),
+ * choice_bias [E] fp32 or NULL -> topk_idx [T][k] int32, topk_w [T][k] fp32, as
+ * afd_ffn_dispatch_rows and afd_ffn_combine_rows take them.  E <= 256, k <= min(E, 32).  No
+ * handle, no workspace, one launch on `stream`; capturable. */
+int afd_ffn_select_experts(const void *logits, int32_t logits_dtype, int64_t logits_stride,
+                           const float *choice_bias, int32_t T, int32_t E, int32_t k,
+                           const afd_ffn_routing *routing, int32_t *topk_idx, float *topk_w, void *stream);
+
+/* Make afd_ffn_route and every afd_ffn_forward* of the handle select and weigh experts this way
+ * (the handle's router_bias, if any, is part of the logits).  choice_bias [E] fp32 (device) or
+ * NULL: borrowed, read by each later call, must outlive them.  routing is copied; NULL (with
+ * choice_bias NULL) restores the softmax top-k.  Host only; a graph captured before keeps the
+ * routing it was captured with. */
+int afd_ffn_set_routing(afd_ffn_handle *h, const afd_ffn_routing *routing, const float *choice_bias);
 
 /* Dispatch order and dispatched rows: each token's hidden state is sent to the experts it
  * chose (A/F 分离 page, section 机制, the dispatch step).  From topk_idx [T][k]:
@@ -286,6 +326,69 @@ int afd_ffn_expert_rows_fp8(afd_ffn_handle *h, const void *rows, const float *ro
  * 16-byte aligned. */
 int afd_ffn_combine_rows_bf16(const void *Y, const void *Ys, const float *topk_w, const int32_t *pos, int32_t T,
                               int32_t k, int32_t H, void *out, void *stream);
+
+/* ---- 4-bit experts ------------------------------------------------------------------
+ * Rows grouped by expert times weights in 4 bits with one scale per group of `group` consecutive
+ * input elements: W[n][k] = (q[n][k] - z[n][k / group]) * scale[n][k / group].  Written for the
+ * few rows an expert gets in a decode micro-batch, where the time is that of streaming the
+ * weights (a quarter of bf16's bytes); it is right, though not fast, for many rows. */
+typedef struct {              /* DEVICE pointers, borrowed, never written                     */
+    const void    *codes;     /* [E][N][K/2] bytes, 16-byte aligned: element k = 2i of a row in
+                                 the low four bits of byte i, k = 2i + 1 in the high four      */
+    const void    *scale;     /* [E][N][K/group] bf16 or fp32                                  */
+    const uint8_t *zero;      /* [E][N][K/group], the low four bits count; NULL = 8 everywhere */
+    int32_t N, K;             /* outputs; inputs, a multiple of 32                             */
+    int32_t group;            /* a multiple of 32 that divides K                               */
+    int32_t scale_dtype;      /* AFD_DT_BF16 or AFD_DT_F32                                     */
+} afd_ffn_w4;
+
+/* y[r] = x[r] W_e^T for rows grouped by expert: x [n_rows][K] bf16, counts [E] (device; rows of
+ * expert 0 first, then expert 1, ...) or NULL with E == 1 (one matrix for every row) ->
+ * y [n_rows][N] bf16 or fp32 (y_dtype), summed in fp32 and rounded once.  x, y 16-byte aligned,
+ * y apart from every input.  E <= 256.  Rows behind the last expert's stay as they were.  A
+ * negative count is taken as 0 and rows past n_rows are cut off; both are flagged
+ * (afd_ffn_rows_error).  Asynchronous on `stream`; capturable after one call on the device. */
+int afd_ffn_w4_rows(const afd_ffn_w4 *w, int32_t E, const void *x, const int32_t *counts, int32_t n_rows,
+                    void *y, int32_t y_dtype, void *stream);
+
+/* afd_ffn_expert_rows on 4-bit weights, without a handle: w13 [E][2I][H] (rows 0..I-1 gate,
+ * I..2I-1 up) and w2 [E][H][I], each with its own group, scales and zero points; rows
+ * [n_rows][H] bf16 grouped by expert as counts says -> Y [n_rows][H] bf16 or fp32 (y_dtype), for
+ * afd_ffn_combine_rows_bf16 / afd_ffn_combine_rows.  The SwiGLU output is kept as two bf16 terms
+ * (2^-17 relative).  scratch: afd_ffn_w4_scratch_bytes(n_rows, I) bytes, 16-byte aligned,
+ * caller-owned; calls that can overlap in time (other streams, graphs replayed together) need
+ * a scratch each.  I and H multiples of 32; counts, rows and flags as for afd_ffn_w4_rows. */
+int afd_ffn_w4_expert_rows(const afd_ffn_w4 *w13, const afd_ffn_w4 *w2, int32_t E, const void *rows,
+                           const int32_t *counts, int32_t n_rows, void *Y, int32_t y_dtype, void *scratch,
+                           void *stream);
+
+/* Bytes of that scratch (0 for negative sizes; host only). */
+int64_t afd_ffn_w4_scratch_bytes(int32_t n_rows, int32_t I);
+
+/* ---- residual addition and norm -------------------------------------------------------
+ * The step between the attention output and the FFN: s = x + residual in fp32 (x alone without a
+ * residual), y = s * (mean(s^2) + eps)^(-1/2) * gamma in fp32 from the unrounded s.  Writes
+ *   sum   s in the residual's type, the residual of the next step (NULL: not written; it needs a
+ *         residual); it may be the residual's own buffer, with the same stride
+ *   out   y as bf16, what afd_ffn_route / afd_ffn_forward read (NULL: not written); it may be x's
+ *         own buffer, with the same stride
+ *   codes [T][H] e4m3 and row_scale [T]: y quantised with one scale per row as the W8A8 path
+ *         does (max |y| / 448, 1 for a zero row; nearest even, saturating), what
+ *         afd_ffn_expert_rows_fp8 reads (both NULL: not written)
+ * At least one of out and codes.  Strides are elements from row to row, at least H, 0 = H.  Any
+ * alignment that the types allow is taken; where pointers and row strides are multiples of 16
+ * bytes (codes: 8) and H of 8, rows move as 16-byte vectors.  Buffers must not overlap except
+ * as said.  1 <= H <= 32768.  The sum of squares is in fp32: |s| up to 1e16 is in range.
+ * x, sum, out ... of token t are [t * stride, t * stride + H).  One launch; capturable. */
+typedef struct {
+    int32_t T, H;
+    int32_t residual_dtype;   /* AFD_DT_BF16 or AFD_DT_F32: residual and sum                   */
+    int32_t gamma_dtype;      /* AFD_DT_BF16 or AFD_DT_F32                                     */
+    int64_t x_stride, residual_stride, sum_stride, out_stride;
+    float   eps;              /* finite, >= 0                                                  */
+} afd_ffn_norm_cfg;
+int afd_ffn_add_rmsnorm(const afd_ffn_norm_cfg *cfg, const void *x, const void *residual, const void *gamma,
+                        void *sum, void *out, void *codes, float *row_scale, void *stream);
 
 /* Synchronise the device; AFD_ERR_DEVICE_FLAG if an allocation-free call skipped invalid data
  * since the last check (the word is cleared), else AFD_OK. */

@@ -9,6 +9,7 @@ Modules
 - ``oracle.moe``   router, top-k, gate weights, dispatch order, SwiGLU experts, combine
 - ``oracle.fp8``   e4m3 rounding and the per-row quantisation mirror of the W8A8 path
 - ``oracle.comm``  the pages' per-token dispatch/combine byte account
+- ``oracle.operators``  residual addition and norm, expert selection, 4-bit weights
 
 Pins (every function is checked against something other than itself, in tests marked
 ``not gpu``): closed forms of silu; a hand-derived worked example of one SwiGLU expert
@@ -24,4 +25,4 @@ each one fails its pins.
 The pages print no numeric example of the MoE computation itself, so no pin of the expert
 arithmetic comes from the pages: those pins are mathematical.
 """
-from . import comm, fp8, moe  # noqa: F401
+from . import comm, fp8, moe, operators  # noqa: F401

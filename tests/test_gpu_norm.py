@@ -1,0 +1,178 @@
+"""afd_ffn_add_rmsnorm against the float64 definition.
+
+Bounds, fixed before the first run.  u = 2^-24 is half a step of fp32, relative.
+  sum   fp32: one correctly rounded addition of two values; bf16: half a step of bf16, 2^-8, on top.
+  y     the sum of H squares adds at most 32 terms in a thread, 5 + 5 between lanes and warps, each a
+        step u of a sum of positive terms, 2 more for the square of the rounded s and 1 for the
+        multiply-add: 45 u; mean, + eps, reciprocal root halves that: 23 u + 3 u; two products 2 u,
+        s itself 1 u: 29 u, taken as 32 u.
+  out   + half a step of bf16 (2^-8, relative).
+  scale 32 u + 2 u (the product and the quotient), taken as 40 u.
+  codes |code * scale - y| <= half an e4m3 step (2^-4 of |y|, or 2^-10 of the scale below the
+        normal range) + 80 u |y|.
+"""
+import math
+
+import numpy as np
+import pytest
+import torch
+
+import ffn_side_expert_b200 as afd
+from oracle import operators as op
+
+pytestmark = pytest.mark.gpu
+U = 2.0 ** -24
+BF16, F32 = torch.bfloat16, torch.float32
+DT = {BF16: afd.AFD_DT_BF16, F32: afd.AFD_DT_F32}
+
+
+def f64(t):
+    return t.double().cpu().numpy()
+
+
+def strided(T, H, pad, dtype, gen=None, scale=1.0, fill=7.0):
+    """[T][H] rows of a wider buffer; the gaps hold `fill`."""
+    base = torch.full((T, H + pad), fill, dtype=dtype, device="cuda")
+    rows = base[:, :H]
+    if gen is not None:
+        rows.copy_((scale * torch.randn((T, H), generator=gen)).to(dtype))
+    return base, rows
+
+
+def call(x, r, g, total, out, codes, scale, eps=1e-6, **kw):
+    T, H = x.shape
+    st = lambda t: t.stride(0) if t is not None and T > 1 else 0                # noqa: E731
+    cfg = afd.afd_ffn_norm_cfg(T=T, H=H, residual_dtype=DT[r.dtype] if r is not None else 0, gamma_dtype=DT[g.dtype],
+                               x_stride=st(x), residual_stride=st(r), sum_stride=st(total), out_stride=st(out), eps=eps)
+    assert afd.afd_ffn_add_rmsnorm(cfg, x, r, g, total, out, codes, scale, **kw) == afd.AFD_OK
+
+
+def check(x, r, g, total, out, codes, scale, eps=1e-6):
+    s, y, sc = op.add_rmsnorm(f64(x), f64(r) if r is not None else None, f64(g), eps)
+    if total is not None:
+        half = 2.0 ** -8 if total.dtype == BF16 else 0.0
+        assert (np.abs(f64(total) - s) <= np.abs(s) * (U + half) * (1 + 1e-6)).all()
+    if out is not None:
+        assert (np.abs(f64(out) - y) <= np.abs(y) * (2.0 ** -8 + 33 * U) + 1e-38).all()
+    if codes is not None:
+        assert (np.abs(f64(scale) - sc) <= 40 * U * sc).all()
+        got = f64(codes.float()) * f64(scale)[:, None]
+        step = np.maximum(np.abs(y) * 2.0 ** -4, sc[:, None] * 2.0 ** -10)
+        assert (np.abs(got - y) <= step * (1 + 80 * U) + 80 * U * np.abs(y)).all()
+
+
+@pytest.mark.parametrize("H", [1, 7, 8, 100, 256, 1001, 4097, 7168, 8200, 16383, 32768])
+@pytest.mark.parametrize("rdt,gdt", [(BF16, BF16), (BF16, F32), (F32, BF16), (F32, F32)])
+def test_sizes_and_types(H, rdt, gdt):
+    gen = torch.Generator().manual_seed(H)
+    for T, pad in ((1, 0), (5, 0), (3, 8), (4, 3)):
+        _, x = strided(T, H, pad, BF16, gen)
+        _, r = strided(T, H, pad, rdt, gen, 3.0)
+        g = (1 + 0.3 * torch.randn((H,), generator=gen)).to(gdt).cuda()
+        sb, total = strided(T, H, pad, rdt)
+        ob, out = strided(T, H, pad, BF16)
+        codes = torch.zeros((T, H), dtype=torch.float8_e4m3fn, device="cuda")
+        scale = torch.zeros((T,), device="cuda")
+        call(x, r, g, total, out, codes, scale)
+        check(x, r, g, total, out, codes, scale)
+        for b in (sb, ob):                                      # the gaps between rows stay as they were
+            assert (b[:, H:].float() == 7.0).all()
+
+
+@pytest.mark.parametrize("parts", ["out", "codes", "sum+out", "no residual"])
+def test_optional_parts(parts):
+    gen = torch.Generator().manual_seed(3)
+    T, H = 9, 640
+    _, x = strided(T, H, 0, BF16, gen)
+    _, r = strided(T, H, 0, BF16, gen)
+    g = torch.randn((H,), generator=gen).cuda()
+    out = torch.empty((T, H), dtype=BF16, device="cuda") if parts != "codes" else None
+    codes = torch.empty((T, H), dtype=torch.float8_e4m3fn, device="cuda") if parts == "codes" else None
+    scale = torch.empty((T,), device="cuda") if parts == "codes" else None
+    total = torch.empty_like(r) if parts == "sum+out" else None
+    r = None if parts == "no residual" else r
+    call(x, r, g, total, out, codes, scale)
+    check(x, r, g, total, out, codes, scale)
+
+
+@pytest.mark.parametrize("H", [77, 2048])
+def test_in_place(H):
+    gen = torch.Generator().manual_seed(4)
+    _, x = strided(6, H, 0, BF16, gen)
+    _, r = strided(6, H, 0, BF16, gen)
+    g = torch.ones((H,), device="cuda")
+    x0, r0 = x.clone(), r.clone()
+    call(x, r, g, r, x, None, None)              # sum over the residual, out over x
+    check(x0, r0, g, r, x, None, None)
+
+
+def test_special_rows():
+    """A zero row (scale 1, codes 0), rows with an infinity or a NaN: only those rows are affected."""
+    T, H = 6, 512
+    gen = torch.Generator().manual_seed(5)
+    _, x = strided(T, H, 0, BF16, gen)
+    x[1] = 0
+    x[2, 17] = math.inf
+    x[4, 300] = math.nan
+    g = torch.ones((H,), device="cuda")
+    out = torch.empty((T, H), dtype=BF16, device="cuda")
+    codes = torch.empty((T, H), dtype=torch.float8_e4m3fn, device="cuda")
+    scale = torch.empty((T,), device="cuda")
+    call(x, None, g, None, out, codes, scale)
+    assert scale[1] == 1 and (out[1] == 0).all() and (codes[1].float() == 0).all()
+    assert torch.isnan(out[2, 17]) and (out[2, :17] == 0).all() and torch.isnan(codes[2].float()[17])
+    assert torch.isnan(out[4]).all() and torch.isnan(codes[4].float()).all()
+    ok = [0, 3, 5]
+    check(x[ok], None, g, None, out[ok], codes[ok], scale[ok])
+
+
+def test_unaligned_pointers():
+    """Buffers that start on odd elements take the element path."""
+    T, H = 4, 264
+    gen = torch.Generator().manual_seed(6)
+    x = torch.randn((T * H + 1,), generator=gen).to(BF16).cuda()[1:].view(T, H)
+    r = torch.randn((T * H + 1,), generator=gen).cuda()[1:].view(T, H)
+    g = torch.randn((H + 1,), generator=gen).to(BF16).cuda()[1:]
+    total = torch.empty((T * H + 1,), device="cuda")[1:].view(T, H)
+    out = torch.empty((T * H + 1,), dtype=BF16, device="cuda")[1:].view(T, H)
+    codes = torch.empty((T * H + 1,), dtype=torch.uint8, device="cuda")[1:].view(torch.float8_e4m3fn).view(T, H)
+    scale = torch.empty((T + 1,), device="cuda")[1:]
+    call(x, r, g, total, out, codes, scale)
+    check(x, r, g, total, out, codes, scale)
+
+
+def test_row_offsets_past_32_bits():
+    H, far = 264, (1 << 31) + 16                 # the second row starts 2^31 + 16 elements in
+    buf = torch.empty((far + H,), dtype=BF16, device="cuda")
+    x = buf.as_strided((2, H), (far, 1))
+    gen = torch.Generator().manual_seed(7)
+    x.copy_(torch.randn((2, H), generator=gen).to(BF16))
+    g = torch.ones((H,), device="cuda")
+    out = torch.empty((2, H), dtype=BF16, device="cuda")
+    call(x, None, g, None, out, None, None)
+    check(x, None, g, None, out, None, None)
+
+
+def test_stream_and_graph():
+    gen = torch.Generator().manual_seed(8)
+    T, H = 33, 1024
+    _, x = strided(T, H, 0, BF16, gen)
+    _, r = strided(T, H, 0, BF16, gen)
+    g = torch.randn((H,), generator=gen).cuda()
+    out, total = torch.zeros_like(x), torch.zeros_like(r)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=s):
+            call(x, r, g, total, out, None, None)
+    torch.cuda.synchronize()
+    assert (out == 0).all()
+    x.mul_(2)
+    graph.replay()
+    torch.cuda.synchronize()
+    check(x, r, g, total, out, None, None)
+    again = torch.zeros_like(out)
+    call(x, r, g, total, again, None, None, stream=s)
+    torch.cuda.synchronize()
+    assert torch.equal(out, again)

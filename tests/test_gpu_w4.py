@@ -1,0 +1,327 @@
+"""afd_ffn_w4_rows and afd_ffn_w4_expert_rows against the float64 definition, and the chain
+norm -> selection -> dispatch -> 4-bit experts -> combine.
+
+Bounds, fixed before the first run (u = 2^-24).  The weights q - z and the inputs are exact in bf16
+and their products exact in fp32.  A sum of K products, taken in any order with fp32 accumulators
+(a tensor-core step of 16 products may truncate, 2 u a step) and scaled once per group, is within
+(K / 8 + 32) u of the sum of |x| |W|: K / 16 steps of 2 u at most one after another, one product and
+one addition per group of at least 32 (K / 16 u), the parts' joining (<= 32 u).
+bf16 results: half a step, 2^-8 relative, more.  SwiGLU: |silu'| <= 1.1, so act is within
+1.1 |u| dg + |silu(g)| du + (2^-16 + 2^-20) |act| of the exact one (two bf16 terms: 2^-16 at most;
+expf, quotient and products below 2^-20), which the down product spreads by |W2|.
+"""
+import numpy as np
+import pytest
+import torch
+
+import ffn_side_expert_b200 as afd
+from oracle import moe
+from oracle import operators as op
+
+pytestmark = pytest.mark.gpu
+U = 2.0 ** -24
+BF16, F32 = torch.bfloat16, torch.float32
+
+
+class W4:
+    """Seeded 4-bit weights [E][N][K] on the device and as float64 on the host."""
+
+    def __init__(self, gen, E, N, K, group, zeros=False, scales=BF16):
+        self.codes = torch.randint(0, 256, (E, N, K // 2), dtype=torch.uint8, generator=gen)
+        self.scale = ((0.7 + 0.6 * torch.rand((E, N, K // group), generator=gen)) * (0.22 / K ** 0.5)).to(scales)
+        self.zero = torch.randint(0, 16, (E, N, K // group), dtype=torch.uint8, generator=gen) if zeros else None
+        self.group = group
+        dev = [None if t is None else t.cuda() for t in (self.codes, self.scale, self.zero)]
+        self.plan = afd.w4_weights(*dev, group)
+
+    def __call__(self, e):
+        return op.w4_dequant(self.codes[e].numpy(), self.scale[e].double().numpy(),
+                             None if self.zero is None else self.zero[e].numpy(), self.group)
+
+
+def f64(t):
+    return t.double().cpu().numpy()
+
+
+def rows_of(gen, n, K):
+    return torch.randn((n, K), generator=gen).to(BF16)
+
+
+def rows_tol(a, y, K, dtype):
+    return (K / 8 + 32) * U * a + (2.0 ** -8 * np.abs(y) if dtype == BF16 else U * np.abs(y)) + 1e-38
+
+
+def run_rows(w, E, x, counts, n, dtype, N, spare=3, **kw):
+    y = torch.full((n + spare, N), 7.0, dtype=dtype, device="cuda")
+    c = None if counts is None else torch.tensor(counts, dtype=torch.int32, device="cuda")
+    assert afd.afd_ffn_w4_rows(w.plan, E, x, c, n, y, **kw) == afd.AFD_OK
+    torch.cuda.synchronize()
+    return y
+
+
+def check_rows(w, E, x, counts, dtype, N, K):
+    n = x.shape[0]
+    y = run_rows(w, E, x.cuda(), counts, n, dtype, N)
+    used = n if counts is None else sum(counts)
+    ref, a = op.w4_rows(f64(x), w, [n] if counts is None else counts)
+    err = np.abs(f64(y[:used]) - ref)
+    assert (err <= rows_tol(a, ref, K, dtype)).all(), np.max(err / rows_tol(a, ref, K, dtype))
+    assert (y[used:].float() == 7.0).all()
+    assert afd.afd_ffn_rows_error() == afd.AFD_OK
+
+
+@pytest.mark.parametrize("K,group", [(32, 32), (96, 32), (96, 96), (128, 128), (160, 32), (480, 96), (2080, 32), (7168, 128),
+                                     (7168, 64), (7168, 7168), (1024, 1024), (18432, 128)])
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_one_matrix(K, group, dtype):
+    gen = torch.Generator().manual_seed(K + group)
+    for N, n, zeros, scales in ((1, 1, False, BF16), (40, 3, True, F32), (131, 9, True, BF16), (257, 1, False, F32)):
+        w = W4(gen, 1, N, K, group, zeros, scales)
+        check_rows(w, 1, rows_of(gen, n, K), None, dtype, N, K)
+
+
+@pytest.mark.parametrize("n", [1, 2, 7, 8, 9, 15, 16, 17, 24, 31, 32, 33, 63, 65, 100, 200])
+def test_row_counts_of_one_matrix(n):
+    gen = torch.Generator().manual_seed(n)
+    for group, zeros in ((32, True), (128, False)):
+        w = W4(gen, 1, 200, 640, group, zeros)
+        check_rows(w, 1, rows_of(gen, n, 640), None, F32, 200, 640)
+
+
+@pytest.mark.parametrize("counts", [[0, 3, 0, 1], [5], [0, 0, 0], [1] * 40, [33, 0, 8, 17, 64, 2], [0, 0, 70], [0] * 255 + [2], [1] * 256])
+def test_experts_with_any_rows(counts):
+    gen = torch.Generator().manual_seed(len(counts))
+    E, N, K = len(counts), 72, 256
+    w = W4(gen, E, N, K, 64, True)
+    n = sum(counts)
+    if n == 0:
+        y = run_rows(w, E, rows_of(gen, 4, K).cuda(), counts, 4, F32, N)
+        assert (y == 7.0).all()
+        return
+    check_rows(w, E, rows_of(gen, n, K), counts, F32, N, K)
+    # rows behind the last expert's are left as they were
+    x = rows_of(gen, n + 5, K)
+    y = run_rows(w, E, x.cuda(), counts, n + 5, BF16, N)
+    ref, a = op.w4_rows(f64(x), w, counts)
+    assert (np.abs(f64(y[:n]) - ref) <= rows_tol(a, ref, K, BF16)).all()
+    assert (y[n:].float() == 7.0).all()
+
+
+def test_counts_that_do_not_fit_are_flagged():
+    gen = torch.Generator().manual_seed(1)
+    E, N, K = 3, 64, 128
+    w = W4(gen, E, N, K, 32)
+    x = rows_of(gen, 6, K)
+    for counts, real in (([2, -4, 1], [2, 0, 1]), ([4, 9, 2], [4, 2, 0]), ([2000000000, 2000000000, 1], [6, 0, 0])):
+        y = run_rows(w, E, x.cuda(), counts, 6, F32, N)
+        used = sum(real)
+        ref, a = op.w4_rows(f64(x), w, real)
+        assert (np.abs(f64(y[:used]) - ref) <= rows_tol(a, ref, K, F32)).all()
+        assert (y[used:] == 7.0).all()
+        assert afd.afd_ffn_rows_error() == afd.AFD_ERR_DEVICE_FLAG
+        assert afd.afd_ffn_rows_error() == afd.AFD_OK
+
+
+def test_infinities_and_nans_stay_in_their_rows():
+    gen = torch.Generator().manual_seed(2)
+    w = W4(gen, 2, 64, 256, 64)
+    x = rows_of(gen, 11, 256)
+    x[3, 5] = float("inf")
+    x[7, 200] = float("nan")
+    counts = [6, 5]
+    y = run_rows(w, 2, x.cuda(), counts, 11, F32, 64)
+    clean = x.clone()
+    clean[3], clean[7] = 0, 0
+    ref, a = op.w4_rows(f64(clean), w, counts)
+    ok = [r for r in range(11) if r not in (3, 7)]
+    assert (np.abs(f64(y[:11]) - ref) <= rows_tol(a, ref, 256, F32))[ok].all()
+    assert not torch.isfinite(y[3]).any() and torch.isnan(y[7]).all()
+
+
+def test_extreme_codes_and_zero_points():
+    """Every code and zero point: W of one group is (q - z) exactly."""
+    K = 32
+    q = np.tile(np.arange(16, dtype=np.uint8), (16, 2))
+    w = W4(torch.Generator().manual_seed(0), 1, 16, K, K, True, F32)
+    w.codes = torch.from_numpy(op.w4_pack(q))[None]
+    w.zero = torch.arange(16, dtype=torch.uint8).view(1, 16, 1) + 16 * 5      # the high four bits do not count
+    w.scale = torch.ones((1, 16, 1))
+    w.plan = afd.w4_weights(w.codes.cuda(), w.scale.cuda(), w.zero.cuda(), K)
+    for k in range(K):                                  # a unit row reads one column of the weights
+        x = torch.zeros((1, K), dtype=BF16)
+        x[0, k] = 1
+        y = run_rows(w, 1, x.cuda(), None, 1, F32, 16)
+        assert torch.equal(y[0].cpu(), torch.from_numpy(q[:, k].astype(np.float32) - np.arange(16, dtype=np.float32)))
+
+
+def test_weights_past_32_bits():
+    """Codes of the last expert start more than 2^32 bytes in."""
+    E, N, K = 5, 65536, 32768                            # 1 GiB of codes an expert
+    codes = torch.empty((E, N, K // 2), dtype=torch.uint8, device="cuda")
+    codes.fill_(0x88)
+    codes[4, N - 3:] = torch.randint(0, 256, (3, K // 2), dtype=torch.uint8, device="cuda")
+    scale = torch.full((E, N, K // 1024), 0.01, dtype=BF16, device="cuda")
+    plan = afd.w4_weights(codes, scale, None, 1024)
+    x = rows_of(torch.Generator().manual_seed(3), 1, K)
+    y = torch.full((1, N), 7.0, device="cuda")
+    counts = torch.tensor([0, 0, 0, 0, 1], dtype=torch.int32, device="cuda")
+    assert afd.afd_ffn_w4_rows(plan, E, x.cuda(), counts, 1, y) == afd.AFD_OK
+    torch.cuda.synchronize()
+    w = op.w4_dequant(codes[4, N - 3:].cpu().numpy(), scale[4, N - 3:].double().cpu().numpy(), None, 1024)
+    ref, a = f64(x) @ w.T, np.abs(f64(x)) @ np.abs(w).T
+    assert (np.abs(f64(y[:, N - 3:]) - ref) <= rows_tol(a, ref, K, F32)).all()
+    assert (y[:, :N - 3] == 0).all()
+
+
+# ------------------------------------------------------------------ whole experts
+def experts_tol(x, w13, w2, counts, y, H, I, dtype):
+    gu, a = op.w4_rows(x, w13, counts)
+    d = (H / 8 + 32) * U * a
+    g, u = np.split(gu, 2, axis=1)
+    dg, du = np.split(d, 2, axis=1)
+    act = op.swiglu(gu)
+    silu = moe.silu(g)
+    dact = 1.1 * np.abs(u) * dg + np.abs(silu) * du + 1.1 * dg * du + (2.0 ** -16 + 2.0 ** -20) * np.abs(act)
+    at, tol = 0, []
+    for e, m in enumerate(counts):
+        if m:
+            aw = np.abs(w2(e)).T
+            tol.append((dact[at:at + m] + (I / 8 + 32) * U * (np.abs(act[at:at + m]) + dact[at:at + m])) @ aw)
+            at += m
+    return np.concatenate(tol) + (2.0 ** -8 if dtype == BF16 else U) * np.abs(y) + 1e-38
+
+
+@pytest.mark.parametrize("H,I,g13,g2", [(32, 32, 32, 32), (256, 512, 64, 128), (1056, 96, 32, 96), (2048, 320, 128, 64),
+                                        (7168, 256, 128, 128)])
+@pytest.mark.parametrize("counts", [[1], [0, 2, 0, 1], [9, 0, 40, 1], [1] * 8])
+def test_experts(H, I, g13, g2, counts):
+    gen = torch.Generator().manual_seed(H + I)
+    E, n = len(counts), sum(counts)
+    w13, w2 = W4(gen, E, 2 * I, H, g13, True), W4(gen, E, H, I, g2, False, F32)
+    x = rows_of(gen, n, H)
+    c = torch.tensor(counts, dtype=torch.int32, device="cuda")
+    scratch = torch.full((afd.afd_ffn_w4_scratch_bytes(n + 2, I),), 255, dtype=torch.uint8, device="cuda")
+    ref = op.w4_expert_rows(f64(x), w13, w2, counts)
+    xd = torch.cat([x, x.new_full((2, H), float("nan"))]).cuda()
+    for dtype in (F32, BF16):
+        y = torch.full((n + 2, H), 7.0, dtype=dtype, device="cuda")
+        assert afd.afd_ffn_w4_expert_rows(w13.plan, w2.plan, E, xd, c, n + 2, y, scratch) == afd.AFD_OK
+        torch.cuda.synchronize()
+        tol = experts_tol(f64(x), w13, w2, counts, ref, H, I, dtype)
+        err = np.abs(f64(y[:n]) - ref)
+        assert (err <= tol).all(), np.max(err / tol)
+        assert (y[n:].float() == 7.0).all()
+    assert afd.afd_ffn_rows_error() == afd.AFD_OK
+
+
+def test_experts_with_large_gates():
+    """Gates far beyond expf's range: silu is 0 or the gate itself, never NaN."""
+    gen = torch.Generator().manual_seed(9)
+    H, I = 64, 64
+    w13, w2 = W4(gen, 1, 2 * I, H, 32), W4(gen, 1, H, I, 32)
+    x = (rows_of(gen, 4, H).float() * 1000).to(BF16)
+    y = torch.empty((4, H), device="cuda")
+    scratch = torch.empty((afd.afd_ffn_w4_scratch_bytes(4, I),), dtype=torch.uint8, device="cuda")
+    assert afd.afd_ffn_w4_expert_rows(w13.plan, w2.plan, 1, x.cuda(), None, 4, y, scratch) == afd.AFD_OK
+    torch.cuda.synchronize()
+    ref = op.w4_expert_rows(f64(x), w13, w2, [4])
+    assert (np.abs(f64(y) - ref) <= experts_tol(f64(x), w13, w2, [4], ref, H, I, F32)).all()
+
+
+def test_same_bits_every_time_on_any_stream_and_in_graphs():
+    """Two captured graphs with a scratch each, replayed together on two streams, and plain calls in between."""
+    gen = torch.Generator().manual_seed(10)
+    E, H, I, counts = 6, 512, 256, [3, 0, 20, 1, 9, 2]
+    n = sum(counts)
+    w13, w2 = W4(gen, E, 2 * I, H, 64), W4(gen, E, H, I, 64)
+    c = torch.tensor(counts, dtype=torch.int32, device="cuda")
+    xs = [rows_of(gen, n, H).cuda() for _ in range(2)]
+    size = afd.afd_ffn_w4_scratch_bytes(n, I)
+    scratch = [torch.empty((size,), dtype=torch.uint8, device="cuda") for _ in range(2)]
+    want, ys, graphs, streams = [], [], [], []
+    for i in range(2):
+        y = torch.empty((n, H), dtype=BF16, device="cuda")
+        assert afd.afd_ffn_w4_expert_rows(w13.plan, w2.plan, E, xs[i], c, n, y, scratch[i]) == afd.AFD_OK
+        want.append(y)
+    torch.cuda.synchronize()
+    for i in range(2):
+        s = torch.cuda.Stream()
+        y = torch.zeros((n, H), dtype=BF16, device="cuda")
+        s.wait_stream(torch.cuda.current_stream())
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.stream(s), torch.cuda.graph(graph, stream=s):
+            assert afd.afd_ffn_w4_expert_rows(w13.plan, w2.plan, E, xs[i], c, n, y, scratch[i]) == afd.AFD_OK
+        ys.append(y); graphs.append(graph); streams.append(s)
+    for _ in range(20):
+        for i in range(2):
+            with torch.cuda.stream(streams[i]):
+                graphs[i].replay()
+    torch.cuda.synchronize()
+    assert torch.equal(ys[0], want[0]) and torch.equal(ys[1], want[1])
+
+
+def test_a_row_does_not_depend_on_the_rows_beside_it():
+    """Row by row gives the bits of one call, except that the split of the sums may go by the row count:
+    within twice the sums' bound."""
+    gen = torch.Generator().manual_seed(11)
+    K, N = 1024, 96
+    w = W4(gen, 1, N, K, 128)
+    x = rows_of(gen, 20, K).cuda()
+    whole = run_rows(w, 1, x, None, 20, F32, N)[:20]
+    a = np.abs(f64(x)) @ np.abs(w(0)).T
+    for r in range(20):
+        one = run_rows(w, 1, x[r:r + 1].contiguous(), None, 1, F32, N)[:1]
+        assert (np.abs(f64(one - whole[r:r + 1])) <= 2 * (K / 8 + 32) * U * a[r]).all()
+
+
+# ------------------------------------------------------------------ together
+@pytest.mark.parametrize("T", [1, 5, 64, 300])
+def test_norm_selection_experts_and_combine_together(T):
+    """The FFN half of a layer with 4-bit experts, on device data only, against the float64 chain (the
+    selection's indices taken from the device, their scores held against the definition)."""
+    gen = torch.Generator().manual_seed(20 + T)
+    H, I, E, k, eps = 512, 256, 32, 4, 1e-6
+    x, res = torch.randn((T, H), generator=gen).to(BF16).cuda(), torch.randn((T, H), generator=gen).cuda()
+    gamma = (1 + 0.1 * torch.randn((H,), generator=gen)).cuda()
+    wr = (torch.randn((E, H), generator=gen) / H ** 0.5).cuda()
+    bias = (0.05 * torch.randn((E,), generator=gen)).cuda()
+    w13, w2 = W4(gen, E, 2 * I, H, 128, True), W4(gen, E, H, I, 64)
+    r = dict(sigmoid=True, n_groups=4, topk_groups=2, group_best=2, renormalise=True, weight_scale=2.5)
+
+    total, hidden, out = torch.empty_like(res), torch.empty_like(x), torch.empty_like(x)
+    i32 = lambda *s: torch.empty(s, dtype=torch.int32, device="cuda")                  # noqa: E731
+    idx, w, counts, offsets, pos, src = i32(T, k), torch.empty((T, k), device="cuda"), i32(E), i32(E + 1), i32(T, k), i32(T * k)
+    rows, Y = torch.empty((T * k, H), dtype=BF16, device="cuda"), torch.empty((T * k, H), device="cuda")
+    scratch_d = i32(2 * ((T + 127) // 128) * E)
+    scratch_w = torch.empty((afd.afd_ffn_w4_scratch_bytes(T * k, I),), dtype=torch.uint8, device="cuda")
+    cfg = afd.afd_ffn_norm_cfg(T=T, H=H, residual_dtype=afd.AFD_DT_F32, gamma_dtype=afd.AFD_DT_F32, eps=eps)
+    route = afd.afd_ffn_routing(score=1, n_groups=4, topk_groups=2, group_best=2, renormalise=1, weight_scale=2.5)
+
+    ok = afd.AFD_OK
+    assert afd.afd_ffn_add_rmsnorm(cfg, x, res, gamma, total, hidden) == ok
+    logits = hidden.float() @ wr.T
+    assert afd.afd_ffn_select_experts(logits, bias, T, E, k, route, idx, w) == ok
+    assert afd.afd_ffn_dispatch_rows(hidden, idx, T, k, E, H, counts, offsets, pos, src, rows, scratch_d) == ok
+    assert afd.afd_ffn_w4_expert_rows(w13.plan, w2.plan, E, rows, counts, T * k, Y, scratch_w) == ok
+    assert afd.afd_ffn_combine_rows(Y, None, w, pos, T, k, H, out) == ok
+    torch.cuda.synchronize()
+    assert afd.afd_ffn_rows_error() == ok
+
+    s, y, _ = op.add_rmsnorm(f64(x), f64(res), f64(gamma), eps)
+    assert (np.abs(f64(total) - s) <= U * np.abs(s) * (1 + 1e-6)).all()
+    assert (np.abs(f64(hidden) - y) <= (2.0 ** -8 + 33 * U) * np.abs(y)).all()
+    ri, rw = op.select_experts(f64(logits), f64(bias), k, **r)
+    assert np.array_equal(idx.cpu().numpy(), ri)
+    h = f64(hidden)                                    # what the device's experts read
+    order = np.argsort(ri.reshape(-1), kind="stable")
+    cnt = np.bincount(ri.reshape(-1), minlength=E).tolist()
+    xr = h[order // k]
+    ref_rows = op.w4_expert_rows(xr, w13, w2, cnt)
+    tol_rows = experts_tol(xr, w13, w2, cnt, ref_rows, H, I, F32)
+    yr, tr = np.empty_like(ref_rows), np.empty_like(ref_rows)
+    yr[order], tr[order] = ref_rows, tol_rows
+    yr, tr = yr.reshape(T, k, H), tr.reshape(T, k, H)
+    ref = (rw[:, :, None] * yr).sum(1)
+    # the rows' own error, the weights' (64 u), the sum's (k + 1 steps), half a bf16 step
+    tol = (rw[:, :, None] * (tr + (64 + k + 1) * U * np.abs(yr))).sum(1) * (1 + 2.0 ** -8) + 2.0 ** -8 * np.abs(ref)
+    assert (np.abs(f64(out) - ref) <= tol).all()
