@@ -335,8 +335,9 @@ int afd_ffn_combine_rows_bf16(const void *Y, const void *Ys, const float *topk_w
 typedef struct {              /* DEVICE pointers, borrowed, never written                     */
     const void    *codes;     /* [E][N][K/2] bytes, 16-byte aligned: element k = 2i of a row in
                                  the low four bits of byte i, k = 2i + 1 in the high four      */
-    const void    *scale;     /* [E][N][K/group] bf16 or fp32                                  */
-    const uint8_t *zero;      /* [E][N][K/group], the low four bits count; NULL = 8 everywhere */
+    const void    *scale;     /* [E][N][K/group] bf16 or fp32, 4-byte aligned                  */
+    const uint8_t *zero;      /* [E][N][K/group], 4-byte aligned, the low four bits count;
+                                 NULL = 8 everywhere                                           */
     int32_t N, K;             /* outputs; inputs, a multiple of 32                             */
     int32_t group;            /* a multiple of 32 that divides K                               */
     int32_t scale_dtype;      /* AFD_DT_BF16 or AFD_DT_F32                                     */
@@ -345,7 +346,7 @@ typedef struct {              /* DEVICE pointers, borrowed, never written       
 /* y[r] = x[r] W_e^T for rows grouped by expert: x [n_rows][K] bf16, counts [E] (device; rows of
  * expert 0 first, then expert 1, ...) or NULL with E == 1 (one matrix for every row) ->
  * y [n_rows][N] bf16 or fp32 (y_dtype), summed in fp32 and rounded once.  x, y 16-byte aligned,
- * y apart from every input.  E <= 256.  Rows behind the last expert's stay as they were.  A
+ * y apart from every input.  E <= 256, n_rows <= 2^22.  Rows behind the last expert's stay as they were.  A
  * negative count is taken as 0 and rows past n_rows are cut off; both are flagged
  * (afd_ffn_rows_error).  Asynchronous on `stream`; capturable after one call on the device. */
 int afd_ffn_w4_rows(const afd_ffn_w4 *w, int32_t E, const void *x, const int32_t *counts, int32_t n_rows,

@@ -71,7 +71,8 @@ def check_rows(w, E, x, counts, dtype, N, K):
 
 
 @pytest.mark.parametrize("K,group", [(32, 32), (96, 32), (96, 96), (128, 128), (160, 32), (480, 96), (2080, 32), (7168, 128),
-                                     (7168, 64), (7168, 7168), (1024, 1024), (18432, 128)])
+                                     (7168, 64), (7168, 7168), (1024, 1024), (18432, 128),
+                                     (320, 160), (1440, 160)])
 @pytest.mark.parametrize("dtype", [BF16, F32])
 def test_one_matrix(K, group, dtype):
     gen = torch.Generator().manual_seed(K + group)

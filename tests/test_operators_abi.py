@@ -79,14 +79,14 @@ def _w4(N=64, K=128, group=32, codes=A, scale=A, zero=None, scale_dtype=afd.AFD_
     (dict(N=0), BAD), (dict(K=0), BAD), (dict(K=48), BAD), (dict(group=16), BAD), (dict(group=48), BAD),
     (dict(group=256), BAD), (dict(group=0), BAD), (dict(K=96, group=64), BAD), (dict(scale_dtype=afd.AFD_DT_FP8_E4M3), BAD),
     (dict(codes=None), BAD), (dict(scale=None), BAD), (dict(codes=A + 8), BAD), (dict(scale=A + 1), BAD),
-    (dict(scale=A + 2, scale_dtype=afd.AFD_DT_F32), BAD), (dict(N=1 << 28), NO), (dict(K=1 << 21), NO),
+    (dict(scale=A + 2, scale_dtype=afd.AFD_DT_F32), BAD), (dict(scale=A + 2), BAD), (dict(zero=A + 2), BAD), (dict(N=1 << 28), NO), (dict(K=1 << 21), NO),
 ])
 def test_w4_refuses_weights(w, status):
     assert afd.afd_ffn_w4_rows(_w4(**w), 8, A, A, 4, A, afd.AFD_DT_BF16) == status
 
 
 @pytest.mark.parametrize("kw,status", [
-    (dict(w=None), BAD), (dict(E=0), BAD), (dict(E=257), NO), (dict(n_rows=-1), BAD), (dict(n_rows=(1 << 24) + 1), NO),
+    (dict(w=None), BAD), (dict(E=0), BAD), (dict(E=257), NO), (dict(n_rows=-1), BAD), (dict(n_rows=(1 << 22) + 1), NO),
     (dict(counts=None), BAD), (dict(x=None), BAD), (dict(y=None), BAD), (dict(x=A + 8), BAD), (dict(y=A + 8), BAD),
     (dict(y_dtype=afd.AFD_DT_FP8_E4M3), BAD), (dict(n_rows=0, x=None), OK), (dict(counts=A + 2), BAD),
 ])
