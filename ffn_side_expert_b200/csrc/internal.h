@@ -1,7 +1,10 @@
 // internal.h -- what the library's translation units share on the host side.
 #pragma once
 
+#include <cuda.h>
 #include <cuda_runtime.h>
+
+#include <cstdint>
 
 namespace afd {
 
@@ -10,5 +13,10 @@ int rows_cuda_fail(cudaError_t e);
 
 // The current device's error word of the calls without a handle (afd_ffn_rows_error).
 int rows_err_word(int** out);
+
+// Descriptor of a matrix of `rows` rows of row_bytes bytes (16-byte aligned), boxes of box_rows rows x
+// box_bytes (64) bytes with the 64-byte swizzle, zero fill outside.
+bool encode_byte_rows(CUtensorMap* m, const void* base, uint64_t row_bytes, uint64_t rows, uint32_t box_bytes,
+                      uint32_t box_rows);
 
 }  // namespace afd
