@@ -79,11 +79,23 @@ __device__ __forceinline__ void store_row(float* p, const float (&f)[V]) {
   }
 }
 
-// One CTA per row; thread i takes the pieces of V elements i, i + blockDim, ... (N at most).
-template <int V, int N, typename RT, typename GT>
-__global__ void __launch_bounds__(1024)
+// a / b rounded to nearest, from the correctly rounded reciprocal r of b: one Newton step on the
+// quotient with an exact remainder (P. Markstein, "Computation of elementary functions on the IBM RISC
+// System/6000 processor", 1990).  Holds while neither the quotient nor the remainder leaves the normal
+// range, or the result is far below the last e4m3 code.
+__device__ __forceinline__ float divide(float a, float b, float r) {
+  const float q = a * r;
+  return fmaf(fmaf(-q, b, a), r, q);
+}
+
+// One CTA per row; thread i takes the pieces of V elements i, i + blockDim, ... (N at most) and keeps
+// s gamma in registers; sum is written on the way.  The sum of squares goes through shuffles, the
+// maximum through redux.sync on its bits; then every warp adds the warps' sums in the same order.
+template <int V, int N, int MAXT, int MINB, typename RT, typename GT>
+__global__ void __launch_bounds__(MAXT, MINB)
 add_rmsnorm_kernel(const NormArgs a) {
-  __shared__ float red[2][32];
+  __shared__ float red_sum[32];
+  __shared__ unsigned red_top[32];
   const long long t = blockIdx.x;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const __nv_bfloat16* x = static_cast<const __nv_bfloat16*>(a.x) + t * a.ldx;
@@ -91,13 +103,16 @@ add_rmsnorm_kernel(const NormArgs a) {
   const GT* g = static_cast<const GT*>(a.gamma);
   const int pieces = a.H / V;
   float s[N][V];
-  float ss = 0.f, top = 0.f;
 #pragma unroll
   for (int n = 0; n < N; ++n) {
     const int p = tid + n * blockDim.x;
-    if (p < pieces) {
-      load_row<V>(x + static_cast<size_t>(p) * V, s[n]);
-      if (a.residual) {
+    if (p < pieces) load_row<V>(x + static_cast<size_t>(p) * V, s[n]);
+  }
+  if (a.residual) {
+#pragma unroll
+    for (int n = 0; n < N; ++n) {
+      const int p = tid + n * blockDim.x;
+      if (p < pieces) {
         float rv[V];
         load_row<V>(r + static_cast<size_t>(p) * V, rv);
 #pragma unroll
@@ -105,58 +120,61 @@ add_rmsnorm_kernel(const NormArgs a) {
       }
     }
   }
+  float ss = 0.f, top = 0.f;
 #pragma unroll
   for (int n = 0; n < N; ++n) {
     const int p = tid + n * blockDim.x;
     if (p < pieces) {
+      if (a.sum) store_row<V>(static_cast<RT*>(a.sum) + t * a.lds + static_cast<size_t>(p) * V, s[n]);
       float gv[V];
       load_row<V>(g + static_cast<size_t>(p) * V, gv);
 #pragma unroll
       for (int i = 0; i < V; ++i) {
         ss = fmaf(s[n][i], s[n][i], ss);
-        top = fmaxf(top, fabsf(s[n][i] * gv[i]));
+        s[n][i] *= gv[i];
+        top = fmaxf(top, fabsf(s[n][i]));
       }
-      if (a.sum) store_row<V>(static_cast<RT*>(a.sum) + t * a.lds + static_cast<size_t>(p) * V, s[n]);
     }
   }
   ss = warp_sum(ss);
-  top = warp_max(top);
+  const unsigned wtop = __reduce_max_sync(0xffffffffu, __float_as_uint(top));  // bits of numbers >= 0 are in their order
   if (lane == 0) {
-    red[0][warp] = ss;
-    red[1][warp] = top;
+    red_sum[warp] = ss;
+    red_top[warp] = wtop;
   }
   __syncthreads();
   const int warps = blockDim.x >> 5;
-  ss = warp_sum(lane < warps ? red[0][lane] : 0.f);  // every warp: the same order, the same sum
-  top = warp_max(lane < warps ? red[1][lane] : 0.f);
+  ss = warp_sum(lane < warps ? red_sum[lane] : 0.f);
+  top = __uint_as_float(__reduce_max_sync(0xffffffffu, lane < warps ? red_top[lane] : 0u));
   const float factor = __frsqrt_rn(ss / static_cast<float>(a.H) + a.eps);
   const float amax = top * factor;
   const float scale = amax > 0.f ? __fdiv_rn(amax, kE4m3Max) : 1.0f;
+  const float inv = __frcp_rn(scale);
+  const bool plain = scale > 1e-30f && scale < 1e30f;  // where divide() holds
 #pragma unroll
   for (int n = 0; n < N; ++n) {
     const int p = tid + n * blockDim.x;
     if (p < pieces) {
       float y[V];
-      load_row<V>(g + static_cast<size_t>(p) * V, y);
 #pragma unroll
-      for (int i = 0; i < V; ++i) y[i] = s[n][i] * factor * y[i];
+      for (int i = 0; i < V; ++i) y[i] = s[n][i] * factor;
       if (a.out) store_row<V>(static_cast<__nv_bfloat16*>(a.out) + t * a.ldo + static_cast<size_t>(p) * V, y);
       if (a.codes) {
+#pragma unroll
+        for (int i = 0; i < V; ++i) y[i] = plain ? divide(y[i], scale, inv) : __fdiv_rn(y[i], scale);
         uint8_t* c = a.codes + t * a.H + static_cast<size_t>(p) * V;
         if constexpr (V == 8) {
           uint32_t q[2];
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
             const float* v = y + 4 * i;
-            const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(__fdiv_rn(v[0], scale), __fdiv_rn(v[1], scale)),
-                                                         __NV_SATFINITE, __NV_E4M3);
-            const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(__fdiv_rn(v[2], scale), __fdiv_rn(v[3], scale)),
-                                                         __NV_SATFINITE, __NV_E4M3);
+            const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(v[0], v[1]), __NV_SATFINITE, __NV_E4M3);
+            const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(v[2], v[3]), __NV_SATFINITE, __NV_E4M3);
             q[i] = lo | (hi << 16);
           }
           *reinterpret_cast<uint2*>(c) = make_uint2(q[0], q[1]);
         } else {
-          *c = __nv_cvt_float_to_fp8(__fdiv_rn(y[0], scale), __NV_SATFINITE, __NV_E4M3);
+          *c = __nv_cvt_float_to_fp8(y[0], __NV_SATFINITE, __NV_E4M3);
         }
       }
     }
@@ -164,17 +182,33 @@ add_rmsnorm_kernel(const NormArgs a) {
   if (a.codes && tid == 0) a.row_scale[t] = scale;
 }
 
+template <int V, int N, int MAXT, int MINB, typename RT, typename GT>
+void launch_norm_kernel(const NormArgs& a, int T, cudaStream_t s) {
+  const int threads = (a.H / V + N * 32 - 1) / (N * 32) * 32;
+  add_rmsnorm_kernel<V, N, MAXT, MINB, RT, GT><<<T, threads, 0, s>>>(a);
+}
+
+// Pieces per thread and CTAs per SM.  Few rows: one piece, the shortest way through a row.  Rows that
+// fill the SMs many times: two, so that a row's reduction is paid by fewer warps, in few enough
+// registers that four rows are in flight on an SM.  8192 rows of 7168 (bf16 residual, both outputs):
+// 98 us so (82 % of the copy rate); 1 piece 118 to 122 us, 4 pieces 112 to 139 us, 2 pieces in more
+// registers 110 us.  515 rows of 4097 single elements: 6 a thread 9.1 us, 5 10.7, 8 10.1, 16 13.9 us.
+constexpr int kManyRows = 256;
+
 template <int V, typename RT, typename GT>
 void launch_norm(const NormArgs& a, int T, cudaStream_t s) {
   const int pieces = a.H / V;
-  const int threads = min(1024, (pieces + 31) / 32 * 32);
-  const int n = (pieces + threads - 1) / threads;
-  if (n <= 1)
-    add_rmsnorm_kernel<V, 1, RT, GT><<<T, threads, 0, s>>>(a);
-  else if (n <= 4)
-    add_rmsnorm_kernel<V, 4, RT, GT><<<T, threads, 0, s>>>(a);
-  else if constexpr (V == 1)
-    add_rmsnorm_kernel<V, 32, RT, GT><<<T, threads, 0, s>>>(a);
+  const bool many = T >= kManyRows;
+  if constexpr (V == 8) {
+    if (pieces <= (many ? 128 : 1024)) launch_norm_kernel<V, 1, 1024, 1, RT, GT>(a, T, s);
+    else if (many && pieces <= 1024) launch_norm_kernel<V, 2, 512, 4, RT, GT>(a, T, s);
+    else launch_norm_kernel<V, 4, 1024, 1, RT, GT>(a, T, s);
+  } else {
+    if (pieces <= (many ? 256 : 1024)) launch_norm_kernel<V, 1, 1024, 1, RT, GT>(a, T, s);
+    else if (many && pieces <= 4224) launch_norm_kernel<V, 6, 704, 2, RT, GT>(a, T, s);
+    else if (pieces <= 8192) launch_norm_kernel<V, 8, 1024, 1, RT, GT>(a, T, s);
+    else launch_norm_kernel<V, 32, 1024, 1, RT, GT>(a, T, s);
+  }
 }
 
 template <int V>
