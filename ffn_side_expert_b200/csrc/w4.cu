@@ -38,7 +38,9 @@ constexpr int kBlockRows = 16;     // weight rows of a block (SwiGLU: 8 gate row
 constexpr int kTileBytes = 2 * kBlockRows * kSliceK / 2;
 constexpr int kCols = 8;           // columns of a unit: 8 tokens, or 4 of two planes
 constexpr int kRedPitch = 2 * kBlockRows + 4;
-constexpr int kStages = 4;
+constexpr int kInputBytes = kCols * kSliceK * 2;
+constexpr int kStageBytes = kTileBytes + kInputBytes;
+constexpr int kStages = 3;         // two steps ahead: 64 KB in flight on an SM, and what fits it twice
 
 struct W4Args {
   const uint8_t* codes;
@@ -49,7 +51,8 @@ struct W4Args {
   void* y;
   int E, N, K, G, n_rows, scale_f32, y_f32;
   unsigned group_inv;       // ceil(2^32 / (G / 32)), 0 for groups of 32
-  int windows;              // rows of scales (and zero points) that whole 16-byte pieces cover
+  int glog;                 // log2 G, where windows says so
+  int windows;              // groups of 2^i, rows of scales (and zero points) that whole 16-byte pieces cover
   int* err;
 };
 
@@ -88,6 +91,13 @@ __device__ __forceinline__ uint32_t fma_bf16x2(uint32_t a, uint32_t b, uint32_t 
   return d;
 }
 
+// a & b | c
+__device__ __forceinline__ uint32_t and_or(uint32_t a, uint32_t b, uint32_t c) {
+  uint32_t d;
+  asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(d) : "r"(a), "r"(b), "r"(c));
+  return d;
+}
+
 // (q - z) / 4 of a word's eight codes as bf16 pairs: codes i and i + 4 in p[i], or in their own order
 // (OWN_ORDER) codes 2 i and 2 i + 1.  A code in the low four bits of a half, under the exponent of
 // 128, reads 128 + q.  One four bits up reads q 2^-129 as it stands: subnormal up to 7, and the first
@@ -98,15 +108,15 @@ __device__ __forceinline__ void unpack_word(uint32_t w, uint32_t c0, uint32_t c1
   constexpr uint32_t kQuarter = 0x3E803E80u, k2to127 = 0x7F007F00u;
   if (OWN_ORDER) {  // a byte in both halves: its low code from the low half, its high code from the high one
     const uint32_t c = __byte_perm(c0, c1, 0x5410);
-    p[0] = fma_bf16x2((__byte_perm(w, 0, 0x4040) & 0x00f0000fu) | 0x00004300u, 0x7F003E80u, c);
-    p[1] = fma_bf16x2((__byte_perm(w, 0, 0x4141) & 0x00f0000fu) | 0x00004300u, 0x7F003E80u, c);
-    p[2] = fma_bf16x2((__byte_perm(w, 0, 0x4242) & 0x00f0000fu) | 0x00004300u, 0x7F003E80u, c);
-    p[3] = fma_bf16x2((__byte_perm(w, 0, 0x4343) & 0x00f0000fu) | 0x00004300u, 0x7F003E80u, c);
+    p[0] = fma_bf16x2(and_or(__byte_perm(w, 0, 0x4040), 0x00f0000fu, 0x00004300u), 0x7F003E80u, c);
+    p[1] = fma_bf16x2(and_or(__byte_perm(w, 0, 0x4141), 0x00f0000fu, 0x00004300u), 0x7F003E80u, c);
+    p[2] = fma_bf16x2(and_or(__byte_perm(w, 0, 0x4242), 0x00f0000fu, 0x00004300u), 0x7F003E80u, c);
+    p[3] = fma_bf16x2(and_or(__byte_perm(w, 0, 0x4343), 0x00f0000fu, 0x00004300u), 0x7F003E80u, c);
   } else {
     const uint32_t s = w >> 8;
-    p[0] = fma_bf16x2((w & 0x000f000fu) | 0x43004300u, kQuarter, c0);
+    p[0] = fma_bf16x2(and_or(w, 0x000f000fu, 0x43004300u), kQuarter, c0);
     p[1] = fma_bf16x2(w & 0x00f000f0u, k2to127, c1);
-    p[2] = fma_bf16x2((s & 0x000f000fu) | 0x43004300u, kQuarter, c0);
+    p[2] = fma_bf16x2(and_or(s, 0x000f000fu, 0x43004300u), kQuarter, c0);
     p[3] = fma_bf16x2(s & 0x00f000f0u, k2to127, c1);
   }
 }
@@ -218,246 +228,10 @@ __device__ __forceinline__ void store_out(const W4Args& a, int row, int out, int
 }  // namespace afd
 
 #include "w4_wide.cuh"
+#include "w4_narrow.cuh"
 
 namespace afd {
 namespace {
-
-// Warps that share a unit.  A team's cost: its units, two blocks at 10 or one at 6, times the steps
-// of a warp and about 0.8 of a step for the join.  The smallest wins, the wider split on a tie.
-__device__ __forceinline__ int choose_split(int blocks, int slices, int ctas) {
-  int best = 8, least = 0x7fffffff;
-  for (int split = 8; split >= 1; split >>= 1) {
-    const int teams = ctas * (kWarps / split);
-    const int n = (blocks + teams - 1) / teams;
-    const long long cost = static_cast<long long>((n >> 1) * 10 + (n & 1) * 6) * ((slices + split - 1) / split * 10 + 8);
-    if (cost < least) {
-      least = static_cast<int>(cost);
-      best = split;
-    }
-  }
-  return best;
-}
-
-// The experts with few rows: at most kCols columns.
-// PARTS: groups of a slice with a scale each (1, 2 or 4).
-template <int MODE, int PARTS, bool ZERO>
-__global__ void __launch_bounds__(kThreads, 2) w4_rows_kernel(const W4Args a) {
-  constexpr bool SWIGLU = MODE == kGateUp, WIDE = PARTS == 1;
-  constexpr int kPlanes = MODE == kDown ? 2 : 1;
-  constexpr int kOut = SWIGLU ? kBlockRows / 2 : kBlockRows;  // outputs of a block
-  extern __shared__ __align__(16) uint8_t ring[];             // [kWarps][kStages][kTileBytes]
-  __shared__ float red[2][kWarps][kCols][kRedPitch];
-  __shared__ UnitTables tb;
-  __shared__ int wsum[kWarps];
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int g = lane >> 2, t = lane & 3;
-  launch_dependents();
-  const int outs = SWIGLU ? a.N / 2 : a.N;
-  const int per_expert = (outs + kOut - 1) / kOut;
-  build_tables(a, [&](int rows) { return rows > 0 && rows * kPlanes <= kCols ? per_expert : 0; }, tb, wsum);
-  const int total = tb.unit_base[a.E];
-  const int KG = a.K / a.G;
-  // split warps share a unit, each with every split-th slice of K; a team takes consecutive blocks
-  const int slices = (a.K + kSliceK - 1) / kSliceK;
-  const int split = choose_split(total, slices, gridDim.x);
-  const int sub = warp & (split - 1), team = warp / split;
-  const int active = min(split, slices);                     // warps of a team with a slice
-  const int steps = (slices - sub + split - 1) / split;      // this warp's slices of a unit
-  const int teams = gridDim.x * (kWarps / split), me = blockIdx.x * (kWarps / split) + team;
-  const int b0 = static_cast<int>(static_cast<long long>(total) * me / teams);
-  const int b1 = static_cast<int>(static_cast<long long>(total) * (me + 1) / teams);
-  const int cps = a.scale_f32 ? 4 : 2;
-
-  // ---- loads: a step is the unit's rows x 128 inputs
-  // Row r's 16 bytes c are kept at place c ^ (r / 2 % 4), so that neither side's accesses conflict.
-  const int swizzle = (g >> 1) & 3;
-  uint8_t* const my_ring = ring + warp * kStages * kTileBytes + g * 64;
-  const uint32_t put = smem_u32(my_ring) + (t ^ swizzle) * 16;
-  int lb = steps > 0 ? b0 : b1, ls = 0, le = 0, lmt = 0, lslot = 0;
-  const uint8_t* wp[4];
-  auto load_step = [&]() {
-    if (lb < b1) {
-      if (ls == 0) {
-        const Unit un = unit_at<SWIGLU>(lb, b1, &le, tb);
-        lmt = un.mt;
-        const size_t row = static_cast<size_t>(un.e) * a.N;
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-          wp[i] = a.codes + (row + weight_row<SWIGLU>(a, un.row0, i, g)) * (a.K / 2) + sub * 64 + t * 16;
-        // the scales and zero points of row `lane`, which the products read: in L2 by then
-        const size_t at = (row + weight_row<SWIGLU>(a, un.row0, lane >> 3, lane & 7)) * KG;
-        const uint8_t* sp = static_cast<const uint8_t*>(a.scale) + at * cps;
-        if (lane < un.mt * kBlockRows) {
-          for (int o = sub * 32; o < KG * cps; o += split * 32) prefetch_l2(sp + o);
-          if (ZERO)
-            for (int o = sub * 32; o < KG; o += split * 32) prefetch_l2(a.zero + at + o);
-        }
-      }
-      const uint32_t dst = put + lslot;
-      const bool in = WIDE || (ls * split + sub) * kSliceK + t * 32 < a.K;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        if (i == 2 && lmt == 1) break;
-        if (WIDE)
-          cp_async16(dst + i * 512, wp[i]);
-        else
-          cp_async16(dst + i * 512, in ? wp[i] : a.codes, in);
-        wp[i] += split * 64;
-      }
-      if (++ls == steps) {
-        ls = 0;
-        lb += lmt;
-      }
-    }
-    cp_async_commit();
-    lslot = lslot == (kStages - 1) * kTileBytes ? 0 : lslot + kTileBytes;
-  };
-
-#pragma unroll 1
-  for (int i = 0; i < kStages - 1; ++i) load_step();
-  if (MODE == kDown) wait_dependency();
-
-  int ce = 0, cslot = 0, buf = 0;
-  for (int b = b0; b < b1; buf ^= 1) {
-    const Unit un = unit_at<SWIGLU>(b, b1, &ce, tb);
-    b += un.mt;
-    const int cols = un.m * kPlanes;
-    auto products = [&](auto blocks) {
-      constexpr int MT = decltype(blocks)::value;
-      // columns past the last one repeat it; their results are not used
-      const __nv_bfloat16* col = a.x + (static_cast<size_t>(un.first) * kPlanes + min(g, cols - 1)) * a.K + sub * kSliceK + t * (WIDE ? 32 : 8);
-      // scales of rows i * 8 + g
-      const uint8_t* sp[2 * MT];
-      const uint8_t* zp[ZERO ? 2 * MT : 1];
-#pragma unroll
-      for (int i = 0; i < 2 * MT; ++i) {
-        const size_t at = (static_cast<size_t>(un.e) * a.N + weight_row<SWIGLU>(a, un.row0, i, g)) * KG;
-        sp[i] = static_cast<const uint8_t*>(a.scale) + at * cps;
-        if (ZERO) zp[i] = a.zero + at;
-      }
-      float acc[MT][4];
-#pragma unroll
-      for (int i = 0; i < MT * 4; ++i) (&acc[0][0])[i] = 0.f;
-
-#pragma unroll 1
-      for (int s = 0, k = sub * kSliceK; s < steps; ++s, k += split * kSliceK) {
-        const uint8_t* slot = my_ring + cslot;
-        cslot = cslot == (kStages - 1) * kTileBytes ? 0 : cslot + kTileBytes;
-        const int parts = WIDE ? 4 : min(4, (a.K - k) / 32);
-        uint4 x[4];
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-          if (WIDE || j < parts) x[j] = *reinterpret_cast<const uint4*>(col + j * (WIDE ? 8 : 32));
-        col += split * kSliceK;
-        float sc[2 * MT];
-        uint32_t z[2 * MT];
-        auto load_scales = [&](int j) {
-          const int d = group_of(a, k / 32 + j);
-          if (a.scale_f32) {
-#pragma unroll
-            for (int i = 0; i < 2 * MT; ++i) sc[i] = __ldg(reinterpret_cast<const float*>(sp[i]) + d);
-          } else {
-#pragma unroll
-            for (int i = 0; i < 2 * MT; ++i)
-              sc[i] = __uint_as_float(static_cast<uint32_t>(__ldg(reinterpret_cast<const unsigned short*>(sp[i]) + d)) << 16);
-          }
-          if (ZERO) {
-#pragma unroll
-            for (int i = 0; i < 2 * MT; ++i) z[i] = __ldg(zp[i] + d);
-          }
-        };
-        load_scales(0);
-        cp_async_wait<kStages - 2>();
-        __syncwarp();
-        load_step();
-        uint4 wide[2 * MT];
-        if (WIDE) {
-#pragma unroll
-          for (int i = 0; i < 2 * MT; ++i) wide[i] = *reinterpret_cast<const uint4*>(slot + i * 512 + (t ^ swizzle) * 16);
-        }
-        float part[MT][4], f[2 * MT];
-        const float none[4] = {0.f, 0.f, 0.f, 0.f};
-        uint32_t c0[2 * MT], c1[2 * MT];
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          if (!WIDE && j >= parts) break;
-          constexpr int kSpan = 4 / PARTS;  // words of a part
-          const bool starts = j % kSpan == 0, ends = j % kSpan == kSpan - 1;
-          if (starts) {
-#pragma unroll
-            for (int i = 0; i < 2 * MT; ++i) {
-              c0[i] = 0xC208C208u;  // -(128 + 8) / 4
-              c1[i] = 0xC000C000u;  // -8 / 4
-              if (ZERO) {
-                const uint32_t q = ((z[i] & 15u) | 0x4300u) * 0x10001u;  // 128 + z
-                c0[i] = fma_bf16x2(q, 0xBE80BE80u, 0x80008000u);
-                c1[i] = fma_bf16x2(q, 0xBE80BE80u, 0x42004200u);
-              }
-              f[i] = sc[i];
-            }
-            if (j + kSpan < 4 && j + kSpan < parts) load_scales(j + kSpan);
-          }
-          uint32_t p[2 * MT][4];
-#pragma unroll
-          for (int i = 0; i < 2 * MT; ++i) {
-            const uint32_t w = WIDE ? (j == 0 ? wide[i].x : j == 1 ? wide[i].y : j == 2 ? wide[i].z : wide[i].w)
-                                    : *reinterpret_cast<const uint32_t*>(slot + i * 512 + (j ^ swizzle) * 16 + t * 4);
-            unpack_word(w, c0[i], c1[i], p[i]);
-          }
-          const uint4 v = x[j];
-          uint32_t x0 = v.x, x1 = v.y, x2 = v.z, x3 = v.w;
-          if (MODE != kDown) {  // inputs i and i + 4 side by side, as the codes
-            x0 = __byte_perm(v.x, v.z, 0x5410);
-            x1 = __byte_perm(v.x, v.z, 0x7632);
-            x2 = __byte_perm(v.y, v.w, 0x5410);
-            x3 = __byte_perm(v.y, v.w, 0x7632);
-          }
-#pragma unroll
-          for (int mt = 0; mt < MT; ++mt) {
-            float(&d)[4] = part[mt];
-            if (starts)
-              mma_bf16(d, p[2 * mt][0], p[2 * mt + 1][0], p[2 * mt][1], p[2 * mt + 1][1], x0, x1, none);
-            else
-              mma_bf16(d, p[2 * mt][0], p[2 * mt + 1][0], p[2 * mt][1], p[2 * mt + 1][1], x0, x1, d);
-            mma_bf16(d, p[2 * mt][2], p[2 * mt + 1][2], p[2 * mt][3], p[2 * mt + 1][3], x2, x3, d);
-            if (ends) {
-#pragma unroll
-              for (int c = 0; c < 4; ++c) acc[mt][c] = fmaf(f[2 * mt + (c >> 1)], d[c], acc[mt][c]);
-            }
-          }
-        }
-      }
-      if (sub < active) {
-#pragma unroll
-        for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-          for (int c = 0; c < 4; ++c) red[buf][warp][t * 2 + (c & 1)][mt * 16 + (c >> 1) * 8 + g] = acc[mt][c];
-      }
-    };
-    if (un.mt == 2) products(std::integral_constant<int, 2>());
-    else products(std::integral_constant<int, 1>());
-
-    // The warps' sums, joined in warp order.  One barrier a unit: a warp that writes this buffer
-    // again has passed the next unit's barrier, and so have all that read it here.
-    asm volatile("bar.sync %0, %1;" ::"r"(team + 1), "r"(split * 32) : "memory");
-    const int w0 = team * split;
-    auto sum = [&](int tok, int row) {
-      float v = 0.f;
-      for (int w = 0; w < active; ++w) {
-#pragma unroll
-        for (int p = 0; p < kPlanes; ++p) v += red[buf][w0 + w][tok * kPlanes + p][row];
-      }
-      return v * 4.f;
-    };
-    const int unit_outs = un.mt * kOut;
-    for (int o = sub * 32 + lane; o < un.m * 2 * kOut; o += split * 32) {
-      const int tok = o / (2 * kOut), out = o % (2 * kOut);
-      if (out >= unit_outs || un.row0 + out >= outs) continue;
-      store_out<MODE>(a, un.first + tok, un.row0 + out, outs, sum(tok, SWIGLU ? (out >> 3) * 16 + (out & 7) : out),
-                      SWIGLU ? sum(tok, (out >> 3) * 16 + 8 + (out & 7)) : 0.f);
-    }
-  }
-}
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
@@ -485,7 +259,7 @@ int check_w4_pointers(const afd_ffn_w4* w) {
   return AFD_OK;
 }
 
-constexpr int kRingBytes = kWarps * kStages * kTileBytes;
+constexpr int kRingBytes = kWarps * kStages * kStageBytes;
 constexpr int kMaxDevices = 64;
 
 // A kernel's launch on the current device; at most one of the stream's kernels may still run when it
@@ -517,24 +291,17 @@ cudaError_t launch_on_device(void (*kernel)(Args...), std::atomic<int>* sm_count
   return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
-template <int MODE, int PARTS, bool ZERO>
-cudaError_t launch_few(const W4Args& a, bool programmatic, cudaStream_t s) {
-  static std::atomic<int> sm_count[kMaxDevices];
-  return launch_on_device(w4_rows_kernel<MODE, PARTS, ZERO>, sm_count, 2, kThreads, kRingBytes, programmatic, s, a);
-}
-
 template <int MODE, int PARTS>
 cudaError_t launch_wide(const CUtensorMap& codes, const W4Args& a, bool programmatic, cudaStream_t s) {
   static std::atomic<int> sm_count[kMaxDevices];
   return launch_on_device(w4_wide_kernel<MODE, PARTS>, sm_count, 1, kWideThreads, kWideSmem, programmatic, s, codes, a);
 }
 
-template <int MODE, int PARTS>
-cudaError_t launch_parts(const W4Args& a, bool few, const CUtensorMap* more, bool after, cudaStream_t s) {
-  cudaError_t e = cudaSuccess;
-  if (few) e = a.zero ? launch_few<MODE, PARTS, true>(a, after, s) : launch_few<MODE, PARTS, false>(a, after, s);
-  if (more && e == cudaSuccess) e = launch_wide<MODE, PARTS>(*more, a, after || few, s);
-  return e;
+template <int MODE, int PARTS, int S>
+cudaError_t launch_narrow(const NarrowMaps& codes, const W4Args& a, bool programmatic, cudaStream_t s) {
+  static std::atomic<int> sm_count[kMaxDevices];
+  return launch_on_device(w4_narrow_kernel<MODE, PARTS, S>, sm_count, 1, Narrow<S>::kThreads, Narrow<S>::kSmem, programmatic,
+                          s, codes, a);
 }
 
 // One product: the experts with few rows, then those with more.  Only a call that can have such
@@ -557,18 +324,31 @@ int launch_w4(const afd_ffn_w4& w, int E, const void* x, const int32_t* counts, 
   a.group_inv = q == 1 ? 0u : static_cast<unsigned>(((1ull << 32) + q - 1) / q);
   // groups that 16 bytes of scales hold; a slice's groups lie in one such piece where slices and groups nest
   const int piece = a.scale_f32 ? 4 : 8;
-  a.windows = a.K / a.G % piece == 0 && (w.group % kSliceK == 0 || kSliceK % w.group == 0) && aligned16(w.scale) &&
+  a.windows = a.K / a.G % piece == 0 && (w.group & (w.group - 1)) == 0 && aligned16(w.scale) &&
               (reinterpret_cast<uintptr_t>(w.zero) & (piece - 1)) == 0;
+  while (a.glog < 31 && 1 << (a.glog + 1) <= w.group) ++a.glog;
   a.err = err;
-  const bool more = static_cast<long long>(n_rows) * kPlanes > kCols;
-  CUtensorMap map;
-  if (more && !encode_byte_rows(&map, w.codes, w.K / 2, static_cast<uint64_t>(E) * w.N, kSliceK / 2, kWideRows / 2))
-    return AFD_ERR_NO_DEVICE;
-  const bool few = !more || counts;
-  const CUtensorMap* m = more ? &map : nullptr;
-  const cudaError_t e = w.group % 128 == 0  ? launch_parts<MODE, 1>(a, few, m, after, s)
-                        : w.group % 64 == 0 ? launch_parts<MODE, 2>(a, few, m, after, s)
-                                            : launch_parts<MODE, 4>(a, few, m, after, s);
+  const bool more = static_cast<long long>(n_rows) * kPlanes > kNarrowN;
+  const uint64_t row_bytes = w.K / 2, rows = static_cast<uint64_t>(E) * w.N;
+  cudaError_t e = cudaSuccess;
+  if (!more || counts) {
+    const bool wide = w.group % 128 == 0;  // steps of 256 inputs
+    NarrowMaps maps;
+    for (int i = 0; i < 3; ++i)
+      if (!encode_byte_rows(&maps.map[i], w.codes, row_bytes, rows, wide ? 128 : 64, 64 >> i)) return AFD_ERR_NO_DEVICE;
+    e = w.group % 256 == 0  ? launch_narrow<MODE, 1, 256>(maps, a, after, s)
+        : wide              ? launch_narrow<MODE, 2, 256>(maps, a, after, s)
+        : w.group % 64 == 0 ? launch_narrow<MODE, 2, 128>(maps, a, after, s)
+                            : launch_narrow<MODE, 4, 128>(maps, a, after, s);
+    after = true;
+  }
+  if (more && e == cudaSuccess) {
+    CUtensorMap map;
+    if (!encode_byte_rows(&map, w.codes, row_bytes, rows, kSliceK / 2, kWideRows / 2)) return AFD_ERR_NO_DEVICE;
+    e = w.group % 128 == 0  ? launch_wide<MODE, 1>(map, a, after, s)
+        : w.group % 64 == 0 ? launch_wide<MODE, 2>(map, a, after, s)
+                            : launch_wide<MODE, 4>(map, a, after, s);
+  }
   return e == cudaSuccess ? AFD_OK : rows_cuda_fail(e);
 }
 

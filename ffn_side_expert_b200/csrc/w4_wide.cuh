@@ -18,6 +18,7 @@
 
 namespace afd {
 
+constexpr int kManyCols = 16;  // more columns than this: here; up to it: w4_narrow.cuh
 constexpr int kWgs = 4, kWideThreads = kWgs * 128;
 constexpr int kWideRows = 128, kWideCols = 64;
 constexpr int kWideStages = 3;
@@ -107,7 +108,7 @@ w4_wide_kernel(const __grid_constant__ CUtensorMap codes, const W4Args a) {
   launch_dependents();
   const int outs = MODE == kGateUp ? a.N / 2 : a.N;
   const int blocks = (outs + kOut - 1) / kOut;
-  build_tables(a, [&](int rows) { return rows * kPlanes > kCols ? (rows + kTokens - 1) / kTokens * blocks : 0; }, tb, wsum);
+  build_tables(a, [&](int rows) { return rows * kPlanes > kManyCols ? (rows + kTokens - 1) / kTokens * blocks : 0; }, tb, wsum);
   const int total = tb.unit_base[a.E];
   if (total == 0) {
     wait_dependency();  // what follows may rely on the kernel before this one
