@@ -53,6 +53,7 @@ struct W4Args {
   unsigned group_inv;       // ceil(2^32 / (G / 32)), 0 for groups of 32
   int glog;                 // log2 G, where windows says so
   int windows;              // groups of 2^i, rows of scales (and zero points) that whole 16-byte pieces cover
+  int above;                // w4_wide.cuh: the experts with more columns than this
   int* err;
 };
 
@@ -67,6 +68,12 @@ __device__ __forceinline__ void cp_async8(uint32_t dst, const void* src) {
 }
 __device__ __forceinline__ void cp_async4(uint32_t dst, const void* src) {
   asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
+}
+// For shared memory that other proxies and warps write: not moved over barriers.
+__device__ __forceinline__ uint4 lds128(uint32_t a) {
+  uint4 v;
+  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a) : "memory");
+  return v;
 }
 __device__ __forceinline__ void prefetch_l2(const void* p) { asm volatile("prefetch.global.L2 [%0];" ::"l"(p)); }
 __device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
@@ -331,7 +338,11 @@ int launch_w4(const afd_ffn_w4& w, int E, const void* x, const int32_t* counts, 
   const bool more = static_cast<long long>(n_rows) * kPlanes > kNarrowN;
   const uint64_t row_bytes = w.K / 2, rows = static_cast<uint64_t>(E) * w.N;
   cudaError_t e = cudaSuccess;
-  if (!more || counts) {
+  // A second kernel takes about 5 us to start, in which 32 MB of codes stream: smaller weights go to one
+  // kernel (16 rows on each of 8 experts of 256 x 512: 26 us with two a product, 17 us with one).
+  const bool small = static_cast<long long>(E) * w.N * (w.K / 2) <= 32 << 20;
+  a.above = small ? 0 : kNarrowN;
+  if (!more || (counts && !small)) {
     const bool wide = w.group % 128 == 0;  // steps of 256 inputs
     NarrowMaps maps;
     for (int i = 0; i < 3; ++i)

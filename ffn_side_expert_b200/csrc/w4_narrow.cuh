@@ -43,26 +43,23 @@ struct NarrowShape {
 };
 
 // The shape of the least cost: a team takes ceil(units / teams) units of ceil(steps / split) steps and
-// about one more for the join.  R rows leave R / 8 columns.
+// about half of one more for the join.  R rows leave R / 8 columns.  A lane works out each candidate: one after
+// another the divisions took 2 us of a kernel's start.
 __device__ __forceinline__ NarrowShape choose_narrow(int experts, int outs, int log_pair, int slices, int ctas, int wgs,
                                                      int cols) {
-  NarrowShape best{7, 1};
-  long long least = -1;
-  for (int lr = 7; lr >= 5; --lr) {
-    if (cols > (1 << lr) / 8) break;
-    const int per = 1 << (lr - log_pair);
-    const long long units = static_cast<long long>(experts) * ((outs + per - 1) / per);
-    const int steps = (slices + (128 >> lr) - 1) >> (7 - lr);
-    for (int split = 1; split <= wgs; split += wgs - 1) {
-      const int teams = ctas * (wgs / split);
-      const long long cost = (units + teams - 1) / teams * ((steps + split - 1) / split * 10 + 6);
-      if (least < 0 || cost < least) {
-        least = cost;
-        best = NarrowShape{lr, split};
-      }
-    }
+  const int lane = threadIdx.x & 31, lr = 7 - (lane >> 1), split = lane & 1 ? wgs : 1;
+  unsigned cost = 0xffffffffu;
+  if (lane < 6 && cols <= (1 << lr) / 8) {
+    const unsigned units = experts * (static_cast<unsigned>(outs + (1 << (lr - log_pair)) - 1) >> (lr - log_pair));
+    const unsigned steps = static_cast<unsigned>(slices + (128 >> lr) - 1) >> (7 - lr);
+    const unsigned teams = ctas * (split == 1 ? wgs : 1);
+    // up to 2^24 in floats, which is enough for a choice, with room for the candidate below it
+    const float c = static_cast<float>((units + teams - 1) / teams) *
+                    static_cast<float>((split == 1 ? steps : (steps + wgs - 1) / static_cast<unsigned>(wgs)) * 10u + 6u);
+    cost = (__float_as_uint(c) & ~31u) | lane;
   }
-  return best;
+  const int best = __reduce_min_sync(0xffffffffu, cost) & 31;
+  return NarrowShape{7 - (best >> 1), best & 1 ? wgs : 1};
 }
 
 // 32 lanes x C columns, waited for.
@@ -260,6 +257,8 @@ w4_narrow_kernel(const __grid_constant__ NarrowMaps codes, const W4Args a) {
     const uint8_t* const zat = gbase + kWindowOff + kZeros + tid * 8;
     const int wlog = a.scale_f32 ? 2 : 3, wmask = (1 << wlog) - 1;
 
+    // this lane's row of a slot, at the place of its first piece; piece c is at ^ (c * 16)
+    const uint32_t codes_at = base + ring_off + r * (S / 2) + (S == 256 ? r & 7 : (r >> 1) & 3) * 16;
     int slot = 0;
     uint32_t full_phase = 0, mma_phase = 0, buf = 0;
     for (int u = u0; u < total; u += teams) {
@@ -383,7 +382,7 @@ w4_narrow_kernel(const __grid_constant__ NarrowMaps codes, const W4Args a) {
           }
         }
         wait(full + 8 * slot, full_phase);
-        const uint8_t* at = gbase + ring_off + slot * L::kStep + r * (S / 2);
+        const uint32_t at = codes_at + slot * L::kStep;
         if (++slot == kStages) {
           slot = 0;
           full_phase ^= 1;
@@ -392,7 +391,7 @@ w4_narrow_kernel(const __grid_constant__ NarrowMaps codes, const W4Args a) {
         uint32_t c0 = 0, c1 = 0;
 #pragma unroll
         for (int c = 0; c < S / 32; ++c) {
-          const uint4 w = *reinterpret_cast<const uint4*>(at + ((c ^ (S == 256 ? r & 7 : (r >> 1) & 3)) * 16));
+          const uint4 w = lds128(at ^ (c * 16));
           if (c % (S / 32 / PARTS) == 0) {
             const uint32_t b = ((z[c * PARTS / (S / 32)] & 15u) | 0x4300u) * 0x10001u;  // 128 + z
             c0 = fma_bf16x2(b, 0xBE80BE80u, 0x80008000u);                        // -(128 + z) / 4

@@ -18,7 +18,6 @@
 
 namespace afd {
 
-constexpr int kManyCols = 16;  // more columns than this: here; up to it: w4_narrow.cuh
 constexpr int kWgs = 4, kWideThreads = kWgs * 128;
 constexpr int kWideRows = 128, kWideCols = 64;
 constexpr int kWideStages = 3;
@@ -54,18 +53,17 @@ __device__ __forceinline__ void group_barrier(int id, int threads) {
 
 // Warpgroups that share a unit, each with its own slices: the split of the least cost, where a team
 // takes ceil(units / teams) units of ceil(slices / split) steps and about 1.5 more for the join.
-__device__ __forceinline__ int choose_wide_split(int units, int slices, int ctas) {
-  int best = kWgs;
-  long long least = -1;
-  for (int split = kWgs; split >= 1; split >>= 1) {
-    const int teams = ctas * (kWgs / split);
-    const long long cost = static_cast<long long>((units + teams - 1) / teams) * ((slices + split - 1) / split * 10 + 15);
-    if (least < 0 || cost < least) {
-      least = cost;
-      best = split;
-    }
+__device__ __forceinline__ int choose_wide_split(unsigned units, unsigned slices, unsigned ctas) {
+  const int lane = threadIdx.x & 31, log = 2 - lane;  // a lane for each candidate
+  static_assert(kWgs == 4, "splits of 4, 2 and 1");
+  unsigned cost = 0xffffffffu;
+  if (lane < 3) {
+    const unsigned teams = ctas * (kWgs >> log);
+    const float c = static_cast<float>((units + teams - 1) / teams) *
+                    static_cast<float>(((slices + (1u << log) - 1) >> log) * 10u + 15u);
+    cost = (__float_as_uint(c) & ~31u) | lane;
   }
-  return best;
+  return kWgs >> (__reduce_min_sync(0xffffffffu, cost) & 31);
 }
 
 struct WideUnit {
@@ -108,7 +106,7 @@ w4_wide_kernel(const __grid_constant__ CUtensorMap codes, const W4Args a) {
   launch_dependents();
   const int outs = MODE == kGateUp ? a.N / 2 : a.N;
   const int blocks = (outs + kOut - 1) / kOut;
-  build_tables(a, [&](int rows) { return rows * kPlanes > kManyCols ? (rows + kTokens - 1) / kTokens * blocks : 0; }, tb, wsum);
+  build_tables(a, [&](int rows) { return rows * kPlanes > a.above ? (rows + kTokens - 1) / kTokens * blocks : 0; }, tb, wsum);
   const int total = tb.unit_base[a.E];
   if (total == 0) {
     wait_dependency();  // what follows may rely on the kernel before this one
