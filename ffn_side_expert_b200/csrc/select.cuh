@@ -13,12 +13,15 @@
 // compared (exactly).  With a bias, or for sums of two scores, neighbours can be closer than the
 // fp32 scores' error; there the fp32 order is taken only where every gap that matters is wider
 // than twice a bound on that error (kScoreErr, kSumErr), and a row with a narrower gap is decided
-// again from scores in 64 bits (exact_order).
+// again from scores in 64 bits: the candidates alone where the groups are sure (order_candidates), else
+// all experts (exact_order).
 //
 // One warp per token, E <= 256: lane l holds the experts l + 32 i.  The logits and choices of a
 // token also sit in 2 KB of shared memory, so that a group (any E / n_groups consecutive
-// experts) can be read by its own 32 / n_groups lanes.  A round of the selection is one
-// redux.sync over order-preserving integer keys and one over the indices.
+// experts) can be read by its own 32 / n_groups lanes.  A lane sorts its
+// eight choices once, as integer keys whose low three bits hold the slot; a round of the selection is one
+// redux.sync over the lanes' first keys, a ballot and a shift in the lane that won.  Keys that agree but for
+// those three bits are told apart by a slower loop over the whole ones.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -43,10 +46,10 @@ struct SelectArgs {
 
 // Bounds on the fp32 scores' error, in steps of 2^-24 and against the largest score of the row.
 // sigmoid 1 / (1 + z): expf's 2 ulp (4 steps) times z / (1 + z) <= 1, the addition 1, the division
-// 1: 6 steps.  softmax: the subtraction |l - max| exp(l - max) <= 0.4, expf 4, the sum's own terms
+// 1: 6 steps = 3.6e-7, taken as 4e-7.  softmax: the subtraction |l - max| exp(l - max) <= 0.4, expf 4, the sum's own terms
 // 4 + 0.4, its 8 additions in a lane and 5 between lanes, the division 1: 23 steps = 1.4e-6, taken
 // as 2e-6.  The sum with the bias rounds by 1 step of |c|, taken as 2.
-constexpr float kScoreErr = 2e-6f;
+constexpr float kSigmoidErr = 4e-7f, kSoftmaxErr = 2e-6f;
 constexpr float kSumErr = 1.2e-7f;
 
 // Order-preserving map of a float to an unsigned integer; 0 is below every number that can occur.
@@ -184,6 +187,34 @@ __device__ __noinline__ int exact_order(const float* logits, double* scratch, co
   return mine;
 }
 
+// The k best in 64 bits of n <= 32 candidates, one a lane (e), which hold them for certain; returns lane
+// j's expert for j < k.  order: 32 ints of the warp's shared memory.
+__device__ __forceinline__ int order_candidates(const float* logits, int* order, const SelectArgs& a, int lane, int n, int e,
+                                                float top) {
+  double sum = 1.0;
+  if (!a.sigmoid) {
+    sum = 0.0;
+    for (int i = lane; i < a.E; i += 32)
+      if (logits[i] > -INFINITY) sum += exp(static_cast<double>(logits[i]) - top);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+  }
+  double c = 0.0;
+  if (lane < n) {
+    const double l = logits[e];
+    c = (a.sigmoid ? 1.0 / (1.0 + exp(-l)) : exp(l - top) / sum) + static_cast<double>(a.choice_bias[e]);
+  }
+  int rank = 0;
+  for (int i = 0; i < n; ++i) {
+    const double oc = __shfl_sync(0xffffffffu, c, i);
+    const int oe = __shfl_sync(0xffffffffu, e, i);
+    rank += oc > c || (oc == c && oe < e);
+  }
+  if (lane < n) order[rank] = e;
+  __syncwarp();
+  return lane < min(a.k, n) ? order[lane] : -1;
+}
+
 constexpr int kSelectWarps = 4;  // tokens per CTA
 
 template <typename LT>
@@ -265,7 +296,7 @@ select_experts_kernel(const SelectArgs a) {
     }
     bmax = warp_max(bmax);
     const float smax = a.sigmoid ? 1.f : 1.f / sum;
-    err = kScoreErr * smax + kSumErr * (smax + bmax);
+    err = (a.sigmoid ? kSigmoidErr : kSoftmaxErr) * smax + kSumErr * (smax + bmax);
   } else {
 #pragma unroll
     for (int i = 0; i < 8; ++i) c[i] = l[i];
@@ -285,7 +316,7 @@ select_experts_kernel(const SelectArgs a) {
     kept = groups_that_stay(schoice, a, lane, &gap);
     if (sums || !by_logit) {
       const float smax = a.sigmoid ? 1.f : 1.f / sum;
-      const float one = by_logit ? (kScoreErr + kSumErr) * smax : err;
+      const float one = by_logit ? ((a.sigmoid ? kSigmoidErr : kSoftmaxErr) + kSumErr) * smax : err;
       sure = gap > 6.f * one;  // two sums of two, and their own rounding
     }
     const int S = a.E / a.n_groups;
@@ -294,33 +325,83 @@ select_experts_kernel(const SelectArgs a) {
     for (int i = 0; i < 8; ++i)
       if (!(kept >> (((lane + 32 * i) * inv) >> 16) & 1u)) c[i] = -INFINITY;
   }
+  const bool groups_sure = sure;
 
+  // the lane's choices, best first: the slot in the low bits, a lower one (a lower index) first
   unsigned key[8];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) key[i] = is_out(c[i]) ? 0u : order_key(c[i]);
-  int mine = -1;
+  for (int i = 0; i < 8; ++i) key[i] = is_out(c[i]) ? 0u : (order_key(c[i]) & ~7u) | (7 - i);
+  auto sort2 = [&](int x, int y) {
+    const unsigned hi = max(key[x], key[y]), lo = min(key[x], key[y]);
+    key[x] = hi;
+    key[y] = lo;
+  };
+  sort2(0, 1); sort2(2, 3); sort2(4, 5); sort2(6, 7); sort2(0, 2); sort2(1, 3); sort2(4, 6); sort2(5, 7);
+  sort2(1, 2); sort2(5, 6); sort2(0, 4); sort2(1, 5); sort2(2, 6); sort2(3, 7); sort2(2, 4); sort2(3, 5);
+  sort2(1, 2); sort2(3, 4); sort2(5, 6);
+  int mine = -1, n = 0;
+  bool told_apart = true, border = true;  // no two keys agree but for the slot; all candidates are taken
   unsigned before = 0u;
-  const int rounds = by_logit ? a.k : a.k + 1;  // one more: the border's gap
+  // bf16 logits: equal but for the slot is equal, and the slot and the lane are the index's order.
+  // Else one round more, for the border; with a bias as many as it takes to leave the error behind.
+  const bool exact_keys = by_logit && sizeof(LT) == 2 && a.logit_bias == nullptr && a.nsplit == 1;
+  const int rounds = by_logit ? a.k + (exact_keys ? 0 : 1) : 33;
   for (int j = 0; j < rounds; ++j) {
-    unsigned m = 0u;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) m = max(m, key[i]);
-    const unsigned best = __reduce_max_sync(0xffffffffu, m);
+    const unsigned best = __reduce_max_sync(0xffffffffu, key[0]);
     if (best == 0u) break;  // uniform: no expert is left
-    unsigned e = 0x7fffffffu;
-#pragma unroll
-    for (int i = 7; i >= 0; --i)
-      if (key[i] == best) e = lane + 32 * i;
-    e = __reduce_min_sync(0xffffffffu, e);
-#pragma unroll
-    for (int i = 0; i < 8; ++i)
-      if (e == static_cast<unsigned>(lane + 32 * i)) key[i] = 0u;
-    if (!by_logit && j > 0) sure = sure && order_value(before) - order_value(best) > 2.f * err;
+    const int winner = __ffs(__ballot_sync(0xffffffffu, key[0] == best)) - 1;
+    if (!by_logit) {
+      if (j > 0) {
+        const float v = order_value(before & ~7u), u = order_value(best & ~7u);
+        const bool apart = v - u > 2.f * err + 0x1p-19f * fmaxf(fabsf(v), fabsf(u));
+        if (j >= a.k && apart) break;
+        if (j == 32) {
+          border = false;
+          break;
+        }
+        sure = sure && apart;
+      }
+    } else if (!exact_keys && j > 0 && (before ^ best) < 8u) {
+      told_apart = false;
+    }
     before = best;
-    if (lane == j && j < a.k) mine = static_cast<int>(e);
+    if (lane == winner) {
+#pragma unroll
+      for (int i = 0; i < 7; ++i) key[i] = key[i + 1];
+      key[7] = 0u;
+    }
+    if (lane == j) mine = winner + 32 * (7 - static_cast<int>(best & 7u));
+    n = j + 1;
+  }
+  if (!told_apart) {  // again, by whole keys
+    mine = -1;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) key[i] = is_out(c[i]) ? 0u : order_key(c[i]);
+    for (int j = 0; j < a.k; ++j) {
+      unsigned m = 0u;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) m = max(m, key[i]);
+      const unsigned best = __reduce_max_sync(0xffffffffu, m);
+      if (best == 0u) break;
+      unsigned e = 0x7fffffffu;
+#pragma unroll
+      for (int i = 7; i >= 0; --i)
+        if (key[i] == best) e = lane + 32 * i;
+      e = __reduce_min_sync(0xffffffffu, e);
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        if (e == static_cast<unsigned>(lane + 32 * i)) key[i] = 0u;
+      if (lane == j) mine = static_cast<int>(e);
+    }
   }
   __syncwarp();  // slog is complete, schoice free again
-  if (!sure) mine = exact_order(slog, s_choice[warp], a, lane);
+  if (!sure || !border) {
+    if (groups_sure && border && !by_logit)
+      mine = order_candidates(slog, reinterpret_cast<int*>(s_choice[warp]), a, lane, n, mine, top);
+    else
+      mine = exact_order(slog, s_choice[warp], a, lane);
+  }
+  if (lane >= a.k) mine = -1;
 
   // gate weights
   const float lm = mine >= 0 ? slog[mine] : -INFINITY;
