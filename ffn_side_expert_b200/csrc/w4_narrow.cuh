@@ -115,7 +115,6 @@ w4_narrow_kernel(const __grid_constant__ NarrowMaps codes, const W4Args a) {
   const int wg = warp >> 2, r = tid & 127;           // warpgroup; TMEM lane
   volatile int* abort = &abort_flag;
 
-  launch_dependents();
   const int outs = MODE == kGateUp ? a.N / 2 : a.N;
   if (tid == 0) most = 0;
   build_tables(a, [&](int rows) { return rows > 0 && rows * kPlanes <= kNarrowN ? 1 : 0; }, tb, wsum);
@@ -147,6 +146,7 @@ w4_narrow_kernel(const __grid_constant__ NarrowMaps codes, const W4Args a) {
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
+  launch_dependents();  // what follows allocates TMEM after this
   const uint32_t tmem = tmem_slot;
   const uint32_t lanes = static_cast<uint32_t>(warp & 3) << 21;  // the warp's lane quarter
   const uint32_t tm_a = tmem + wg * L::kACols, tm_d = tmem + kWgs * L::kACols + wg * L::kAccs;

@@ -103,7 +103,6 @@ w4_wide_kernel(const __grid_constant__ CUtensorMap codes, const W4Args a) {
   const int wg = warp >> 2, r = tid & 127;  // warpgroup; row of the unit, which is the TMEM lane
   volatile int* abort = &abort_flag;
 
-  launch_dependents();
   const int outs = MODE == kGateUp ? a.N / 2 : a.N;
   const int blocks = (outs + kOut - 1) / kOut;
   build_tables(a, [&](int rows) { return rows * kPlanes > a.above ? (rows + kTokens - 1) / kTokens * blocks : 0; }, tb, wsum);
@@ -132,6 +131,7 @@ w4_wide_kernel(const __grid_constant__ CUtensorMap codes, const W4Args a) {
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
+  launch_dependents();  // what follows allocates TMEM after this
   const uint32_t tmem = tmem_slot;
   const uint32_t lanes = static_cast<uint32_t>(warp & 3) << 21;  // the warp's lane quarter
   const uint64_t desc0 = sw128_desc(tokens);

@@ -176,3 +176,40 @@ def test_stream_and_graph():
     call(x, r, g, total, again, None, None, stream=s)
     torch.cuda.synchronize()
     assert torch.equal(out, again)
+
+
+@pytest.mark.parametrize("H", [8, 33, 100, 1001, 1032, 4097, 4096, 5000, 7168, 8192, 8200, 9001])
+@pytest.mark.parametrize("rdt,gdt", [(BF16, F32), (F32, BF16)])
+def test_many_rows(H, rdt, gdt):
+    """Rows enough to fill the SMs many times take other shapes of the kernel."""
+    gen = torch.Generator().manual_seed(H)
+    T = 300
+    for pad in (0, 3):
+        _, x = strided(T, H, pad, BF16, gen)
+        _, r = strided(T, H, pad, rdt, gen, 3.0)
+        g = (1 + 0.3 * torch.randn((H,), generator=gen)).to(gdt).cuda()
+        sb, total = strided(T, H, pad, rdt)
+        ob, out = strided(T, H, pad, BF16)
+        codes = torch.zeros((T, H), dtype=torch.float8_e4m3fn, device="cuda")
+        scale = torch.zeros((T,), device="cuda")
+        call(x, r, g, total, out, codes, scale)
+        check(x, r, g, total, out, codes, scale)
+        for b in (sb, ob):
+            assert (b[:, H:].float() == 7.0).all()
+
+
+@pytest.mark.parametrize("H", [1024, 1025])
+@pytest.mark.parametrize("unit", [1.0, 2.0 ** -90, 2.0 ** -105, 2.0 ** 90, 2.0 ** 110])
+def test_codes_are_those_of_the_quotient(H, unit):
+    """With s = +-1 and eps = 0 the factor is 1 and y is gamma itself: each code is that of gamma / scale,
+    rounded to fp32 first as a division rounds it, over rows of many sizes."""
+    gen = torch.Generator().manual_seed(H)
+    sign = (torch.randint(0, 2, (1, H), generator=gen) * 2 - 1).to(BF16)
+    for _ in range(20):
+        g = (torch.randn((H,), generator=gen) * 2.0 ** torch.randint(-12, 1, (H,), generator=gen)).float() * unit
+        codes = torch.zeros((1, H), dtype=torch.float8_e4m3fn, device="cuda")
+        scale = torch.zeros((1,), device="cuda")
+        call(sign.cuda(), None, g.cuda(), None, None, codes, scale, eps=0.0)
+        y, s = (sign[0].float() * g), scale.cpu()
+        assert s[0] == (g.abs().max() / 448.0)
+        assert torch.equal(codes[0].cpu().float(), (y / s).clamp(-448, 448).to(torch.float8_e4m3fn).float())

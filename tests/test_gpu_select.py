@@ -227,3 +227,26 @@ def test_set_routing_refuses_what_the_handle_cannot():
         assert afd.afd_ffn_set_routing(L.mod.h, None, 4096) == afd.AFD_ERR_INVALID_ARG
     finally:
         L.close()
+
+
+@pytest.mark.parametrize("sigmoid", [False, True])
+@pytest.mark.parametrize("E,k", [(40, 8), (256, 8), (256, 32)])
+def test_more_equal_choices_than_lanes(sigmoid, E, k):
+    """Equal logits, biases a few 1e-9 apart: every expert is a candidate."""
+    rng = np.random.default_rng(11)
+    for trial in range(4):
+        logits = torch.full((3, E), 0.25)
+        logits[1, : E // 2] = -3.0
+        bias = torch.from_numpy((0.3 + 1e-9 * rng.normal(size=E)).astype(np.float32))
+        r = dict(PLAIN, sigmoid=sigmoid, n_groups=1 if trial % 2 else 4, topk_groups=1 if trial % 2 else 4)
+        check(logits.cuda(), bias, k, r)
+
+
+@pytest.mark.parametrize("groups,keep", [(1, 1), (8, 3)])
+def test_logits_that_differ_in_their_last_bits(groups, keep):
+    """fp32 logits next to one another, in every order and with equal ones among them."""
+    rng = np.random.default_rng(12)
+    for at in (1.0, -1.0, 1e-3, -77.0):
+        base = np.float32(at).view(np.int32)
+        l = (base + rng.integers(0, 24, size=(40, 64))).astype(np.int32).view(np.float32)
+        check(torch.from_numpy(l.copy()).cuda(), None, 9, dict(PLAIN, n_groups=groups, topk_groups=keep))

@@ -275,6 +275,86 @@ def test_a_row_does_not_depend_on_the_rows_beside_it():
         assert (np.abs(f64(one - whole[r:r + 1])) <= 2 * (K / 8 + 32) * U * a[r]).all()
 
 
+@pytest.mark.parametrize("K,group,scales", [(4096, 256, BF16), (2048, 512, F32), (2560, 128, F32), (1024, 32, F32),
+                                            (1536, 64, BF16), (2048, 1024, BF16)])
+@pytest.mark.parametrize("n", [1, 4, 6, 13])
+def test_groups_in_whole_pieces(K, group, scales, n):
+    """Rows of scales that 16-byte pieces cover, and the same weights with scales and zero points that start
+    four bytes later, which are read group by group: equal bits."""
+    gen = torch.Generator().manual_seed(K + group + n)
+    N = 144
+    w = W4(gen, 1, N, K, group, True, scales)
+    x = rows_of(gen, n, K)
+    check_rows(w, 1, x, None, F32, N, K)
+    want = run_rows(w, 1, x.cuda(), None, n, F32, N)
+    off = 4 // w.scale.element_size()
+    scale = torch.empty((w.scale.numel() + off,), dtype=scales, device="cuda")[off:].view(w.scale.shape)
+    zero = torch.empty((w.zero.numel() + 4,), dtype=torch.uint8, device="cuda")[4:].view(w.zero.shape)
+    scale.copy_(w.scale)
+    zero.copy_(w.zero)
+    w.plan = afd.w4_weights(w.codes.cuda(), scale, zero, group)
+    assert torch.equal(run_rows(w, 1, x.cuda(), None, n, F32, N), want)
+
+
+@pytest.mark.parametrize("group", [32, 64, 128, 256])
+def test_few_and_many_rows_in_one_call(group):
+    """Weights large enough that experts with few rows and with many go to kernels of their own."""
+    gen = torch.Generator().manual_seed(group)
+    E, N, K, counts = 8, 2304, 4096, [3, 16, 0, 17, 8, 1, 70, 9]
+    w = W4(gen, E, N, K, group, group != 64)
+    n = sum(counts)
+    check_rows(w, E, rows_of(gen, n, K), counts, F32, N, K)
+    few = [2, 0, 4, 1, 0, 0, 8, 1]                       # every expert in few rows: units of 64 and 32 rows
+    check_rows(w, E, rows_of(gen, sum(few), K), few, F32, N, K)
+    ones = [1, 0, 0, 4, 0, 0, 0, 0]
+    check_rows(w, E, rows_of(gen, sum(ones), K), ones, BF16, N, K)
+
+
+@pytest.mark.parametrize("counts", [[1, 0, 9, 4, 33, 8, 2, 5], [1] * 8])
+def test_large_experts_with_few_and_many_rows(counts):
+    gen = torch.Generator().manual_seed(12)
+    E, H, I, n = 8, 4096, 2304, sum(counts)
+    w13, w2 = W4(gen, E, 2 * I, H, 128, True), W4(gen, E, H, I, 64)
+    x = rows_of(gen, n, H)
+    c = torch.tensor(counts, dtype=torch.int32, device="cuda")
+    scratch = torch.empty((afd.afd_ffn_w4_scratch_bytes(n, I),), dtype=torch.uint8, device="cuda")
+    ref = op.w4_expert_rows(f64(x), w13, w2, counts)
+    tol = experts_tol(f64(x), w13, w2, counts, ref, H, I, F32)
+    first = None
+    for _ in range(3):
+        y = torch.full((n, H), 7.0, device="cuda")
+        assert afd.afd_ffn_w4_expert_rows(w13.plan, w2.plan, E, x.cuda(), c, n, y, scratch) == afd.AFD_OK
+        torch.cuda.synchronize()
+        assert (np.abs(f64(y) - ref) <= tol).all()
+        assert first is None or torch.equal(first, y)
+        first = y
+    assert afd.afd_ffn_rows_error() == afd.AFD_OK
+
+
+def test_two_calls_at_once():
+    """Calls on two streams over the same weights, each with rows and scratch of its own."""
+    gen = torch.Generator().manual_seed(13)
+    E, H, I, counts = 4, 1024, 512, [2, 20, 0, 5]
+    n = sum(counts)
+    w13, w2 = W4(gen, E, 2 * I, H, 32, True), W4(gen, E, H, I, 128)
+    c = torch.tensor(counts, dtype=torch.int32, device="cuda")
+    xs = [rows_of(gen, n, H).cuda() for _ in range(2)]
+    scratch = [torch.empty((afd.afd_ffn_w4_scratch_bytes(n, I),), dtype=torch.uint8, device="cuda") for _ in range(2)]
+    ys = [torch.zeros((n, H), dtype=BF16, device="cuda") for _ in range(4)]
+    call = lambda i, y, **kw: afd.afd_ffn_w4_expert_rows(w13.plan, w2.plan, E, xs[i], c, n, y, scratch[i], **kw)  # noqa: E731
+    for i in range(2):
+        assert call(i, ys[i]) == afd.AFD_OK
+        torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    for s in streams:
+        s.wait_stream(torch.cuda.current_stream())
+    for _ in range(30):
+        for i in range(2):
+            assert call(i, ys[2 + i], stream=streams[i]) == afd.AFD_OK
+    torch.cuda.synchronize()
+    assert torch.equal(ys[0], ys[2]) and torch.equal(ys[1], ys[3])
+
+
 # ------------------------------------------------------------------ together
 @pytest.mark.parametrize("T", [1, 5, 64, 300])
 def test_norm_selection_experts_and_combine_together(T):
