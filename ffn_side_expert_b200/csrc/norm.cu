@@ -182,6 +182,158 @@ add_rmsnorm_kernel(const NormArgs a) {
   if (a.codes && tid == 0) a.row_scale[t] = scale;
 }
 
+// Eight elements from p, which has its type's alignment only: the aligned 16-byte pieces that hold them,
+// shifted together.  Only where those lie inside [begin, end), the row; else element by element, where
+// element i counts if first <= i < last.
+__device__ __forceinline__ void shift_words(uint32_t* w, int n, int by) {  // by 0..3 words; n words stay valid
+#pragma unroll
+  for (int i = 0; i < 10; ++i)
+    if (i < n + 2) w[i] = by & 1 ? w[i + 1] : w[i];
+#pragma unroll
+  for (int i = 0; i < 9; ++i)
+    if (i < n) w[i] = by & 2 ? w[i + 2] : w[i];
+}
+template <typename T>
+__device__ __forceinline__ void load_shifted(const T* p, const T* begin, const T* end, int first, int last, float (&f)[8]) {
+  constexpr int kPieces = sizeof(T) == 2 ? 2 : 3;  // that eight elements can touch
+  const uintptr_t a = reinterpret_cast<uintptr_t>(p), from = a & ~static_cast<uintptr_t>(15);
+  const int off = static_cast<int>(a & 15);
+  if (from >= reinterpret_cast<uintptr_t>(begin) &&
+      from + 16 * (off ? kPieces : kPieces - 1) <= reinterpret_cast<uintptr_t>(end)) {
+    uint32_t w[13];
+#pragma unroll
+    for (int i = 0; i < kPieces; ++i) {
+      if (i == kPieces - 1 && !off) break;
+      const uint4 v = reinterpret_cast<const uint4*>(from)[i];
+      w[4 * i] = v.x; w[4 * i + 1] = v.y; w[4 * i + 2] = v.z; w[4 * i + 3] = v.w;
+    }
+    if constexpr (sizeof(T) == 2) {
+      shift_words(w, 5, off >> 2);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const uint32_t v = __funnelshift_r(w[i], w[i + 1], (off & 2) * 8);
+        f[2 * i] = __uint_as_float(v << 16);
+        f[2 * i + 1] = __uint_as_float(v & 0xffff0000u);
+      }
+    } else {
+      shift_words(w, 8, off >> 2);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) f[i] = __uint_as_float(w[i]);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) f[i] = i >= first && i < last ? static_cast<float>(p[i]) : 0.f;
+  }
+}
+
+// Rows that do not start on 16-byte boundaries, written to contiguous tensors: thread i takes the aligned
+// pieces of eight of the outputs, i, i + blockDim, ..., which are aligned pieces of each of them (the flat
+// index is a multiple of eight), and reads its inputs shifted.  A row's first and last piece can reach
+// into its neighbours: those elements are left out.
+template <int N, int MAXT, int MINB, typename RT, typename GT>
+__global__ void __launch_bounds__(MAXT, MINB)
+add_rmsnorm_shifted_kernel(const NormArgs a) {
+  __shared__ float red_sum[32];
+  __shared__ unsigned red_top[32];
+  const long long t = blockIdx.x, flat = t * a.H;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const __nv_bfloat16* x = static_cast<const __nv_bfloat16*>(a.x) + t * a.ldx;
+  const RT* r = static_cast<const RT*>(a.residual) + t * a.ldr;
+  const GT* g = static_cast<const GT*>(a.gamma);
+  const int lead = static_cast<int>(flat & 7), pieces = (lead + a.H + 7) >> 3;
+  float s[N][8];
+#pragma unroll
+  for (int n = 0; n < N; ++n) {
+    const int p = tid + n * blockDim.x;
+    if (p < pieces) {
+      const int e = p * 8 - lead, first = max(0, -e), last = min(8, a.H - e);
+      load_shifted(x + e, x, x + a.H, first, last, s[n]);
+      if (a.residual) {
+        float rv[8];
+        load_shifted(r + e, r, r + a.H, first, last, rv);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) s[n][i] += rv[i];
+      }
+    }
+  }
+  if (a.sum) __syncthreads();  // sum may be the residual's buffer, whose pieces are read by neighbours too
+  // piece p of a row's outputs to v's buffer
+  auto store = [&](auto* to, int p, const float (&v)[8]) {
+    const int e = p * 8 - lead;
+    if (e >= 0 && e + 8 <= a.H) {
+      store_row<8>(to + flat + e, v);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        if (e + i >= 0 && e + i < a.H) {
+          const float one[1] = {v[i]};
+          store_row<1>(to + flat + e + i, one);
+        }
+    }
+  };
+  float ss = 0.f, top = 0.f;
+#pragma unroll
+  for (int n = 0; n < N; ++n) {
+    const int p = tid + n * blockDim.x;
+    if (p < pieces) {
+      const int e = p * 8 - lead;
+      if (a.sum) store(static_cast<RT*>(a.sum), p, s[n]);
+      float gv[8];
+      load_shifted(g + e, g, g + a.H, max(0, -e), min(8, a.H - e), gv);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        ss = fmaf(s[n][i], s[n][i], ss);
+        s[n][i] *= gv[i];
+        top = fmaxf(top, fabsf(s[n][i]));
+      }
+    }
+  }
+  ss = warp_sum(ss);
+  const unsigned wtop = __reduce_max_sync(0xffffffffu, __float_as_uint(top));
+  if (lane == 0) {
+    red_sum[warp] = ss;
+    red_top[warp] = wtop;
+  }
+  __syncthreads();
+  const int warps = blockDim.x >> 5;
+  ss = warp_sum(lane < warps ? red_sum[lane] : 0.f);
+  top = __uint_as_float(__reduce_max_sync(0xffffffffu, lane < warps ? red_top[lane] : 0u));
+  const float factor = __frsqrt_rn(ss / static_cast<float>(a.H) + a.eps);
+  const float amax = top * factor;
+  const float scale = amax > 0.f ? __fdiv_rn(amax, kE4m3Max) : 1.0f;
+  const float inv = __frcp_rn(scale);
+  const bool plain = scale > 1e-30f && scale < 1e30f;
+#pragma unroll
+  for (int n = 0; n < N; ++n) {
+    const int p = tid + n * blockDim.x;
+    if (p < pieces) {
+      float y[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) y[i] = s[n][i] * factor;
+      if (a.out) store(static_cast<__nv_bfloat16*>(a.out), p, y);
+      if (a.codes) {
+        uint32_t q[2] = {0u, 0u};
+#pragma unroll
+        for (int i = 0; i < 8; i += 2) {
+          const float v0 = plain ? divide(y[i], scale, inv) : __fdiv_rn(y[i], scale);
+          const float v1 = plain ? divide(y[i + 1], scale, inv) : __fdiv_rn(y[i + 1], scale);
+          q[i >> 2] |= static_cast<uint32_t>(__nv_cvt_float2_to_fp8x2(make_float2(v0, v1), __NV_SATFINITE, __NV_E4M3)) << (i & 2) * 8;
+        }
+        const int e = p * 8 - lead;
+        uint8_t* c = a.codes + flat + e;
+        if (e >= 0 && e + 8 <= a.H) {
+          *reinterpret_cast<uint2*>(c) = make_uint2(q[0], q[1]);
+        } else {
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+            if (e + i >= 0 && e + i < a.H) c[i] = static_cast<uint8_t>(q[i >> 2] >> (i & 3) * 8);
+        }
+      }
+    }
+  }
+  if (a.codes && tid == 0) a.row_scale[t] = scale;
+}
+
 template <int V, int N, int MAXT, int MINB, typename RT, typename GT>
 void launch_norm_kernel(const NormArgs& a, int T, cudaStream_t s) {
   const int threads = (a.H / V + N * 32 - 1) / (N * 32) * 32;
@@ -206,18 +358,42 @@ void launch_norm(const NormArgs& a, int T, cudaStream_t s) {
   } else {
     if (pieces <= (many ? 256 : 1024)) launch_norm_kernel<V, 1, 1024, 1, RT, GT>(a, T, s);
     else if (many && pieces <= 4224) launch_norm_kernel<V, 6, 704, 2, RT, GT>(a, T, s);
+    else if (many && pieces <= 8192) launch_norm_kernel<V, 8, 1024, 2, RT, GT>(a, T, s);
     else if (pieces <= 8192) launch_norm_kernel<V, 8, 1024, 1, RT, GT>(a, T, s);
     else launch_norm_kernel<V, 32, 1024, 1, RT, GT>(a, T, s);
   }
 }
 
-template <int V>
-void launch_norm_types(const NormArgs& a, const afd_ffn_norm_cfg& c, cudaStream_t s) {
+// Shifted pieces against single elements: 4000 rows of 7001 (fp32 residual, both outputs) 86 us and 151 us,
+// 515 rows of 4097 8.2 and 9.1, 3000 rows of 2345 20 and 29; 8000 rows of 301 13.5 and 10.8.  Four rows on
+// an SM rather than two: 86 against 107 us.
+constexpr int kShiftedMinH = 512;
+
+template <typename RT, typename GT>
+void launch_shifted(const NormArgs& a, int T, cudaStream_t s) {
+  const int pieces = (a.H + 14) / 8;  // at most
+  const int per = pieces <= 256 ? 1 : pieces <= 1024 ? 2 : 5, threads = (pieces + per * 32 - 1) / (per * 32) * 32;
+  if (per == 1) add_rmsnorm_shifted_kernel<1, 256, 4, RT, GT><<<T, threads, 0, s>>>(a);
+  else if (per == 2) add_rmsnorm_shifted_kernel<2, 512, 4, RT, GT><<<T, threads, 0, s>>>(a);
+  else add_rmsnorm_shifted_kernel<5, 1024, 1, RT, GT><<<T, threads, 0, s>>>(a);
+}
+
+// How rows move: 16-byte pieces, shifted pieces, single elements.
+enum NormForm { kPieces, kShifted, kElements };
+
+template <typename RT, typename GT>
+void launch_norm_form(const NormArgs& a, int T, NormForm form, cudaStream_t s) {
+  if (form == kPieces) launch_norm<8, RT, GT>(a, T, s);
+  else if (form == kShifted) launch_shifted<RT, GT>(a, T, s);
+  else launch_norm<1, RT, GT>(a, T, s);
+}
+
+void launch_norm_types(const NormArgs& a, const afd_ffn_norm_cfg& c, NormForm form, cudaStream_t s) {
   const bool rf = c.residual_dtype == AFD_DT_F32, gf = c.gamma_dtype == AFD_DT_F32;
-  if (rf && gf) launch_norm<V, float, float>(a, c.T, s);
-  else if (rf) launch_norm<V, float, __nv_bfloat16>(a, c.T, s);
-  else if (gf) launch_norm<V, __nv_bfloat16, float>(a, c.T, s);
-  else launch_norm<V, __nv_bfloat16, __nv_bfloat16>(a, c.T, s);
+  if (rf && gf) launch_norm_form<float, float>(a, c.T, form, s);
+  else if (rf) launch_norm_form<float, __nv_bfloat16>(a, c.T, form, s);
+  else if (gf) launch_norm_form<__nv_bfloat16, float>(a, c.T, form, s);
+  else launch_norm_form<__nv_bfloat16, __nv_bfloat16>(a, c.T, form, s);
 }
 
 bool elem_dtype(int32_t d) { return d == AFD_DT_BF16 || d == AFD_DT_F32; }
@@ -255,7 +431,10 @@ extern "C" int afd_ffn_add_rmsnorm(const afd_ffn_norm_cfg* cfg, const void* x, c
                     (!sum || (aligned(sum, 16) && a.lds % rper == 0)) &&
                     (!out || (aligned(out, 16) && a.ldo % 8 == 0)) && (!codes || aligned(codes, 8));
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  if (wide) launch_norm_types<8>(a, c, s); else launch_norm_types<1>(a, c, s);
+  // Outputs without gaps between their rows, from a 16-byte boundary on.
+  const bool flat = (!sum || (a.lds == c.H && aligned(sum, 16))) && (!out || (a.ldo == c.H && aligned(out, 16))) &&
+                    (!codes || aligned(codes, 8));
+  launch_norm_types(a, c, wide ? kPieces : flat && c.H >= kShiftedMinH ? kShifted : kElements, s);
   const cudaError_t e = cudaGetLastError();
   return e == cudaSuccess ? AFD_OK : rows_cuda_fail(e);
 }

@@ -213,3 +213,38 @@ def test_codes_are_those_of_the_quotient(H, unit):
         y, s = (sign[0].float() * g), scale.cpu()
         assert s[0] == (g.abs().max() / 448.0)
         assert torch.equal(codes[0].cpu().float(), (y / s).clamp(-448, 448).to(torch.float8_e4m3fn).float())
+
+
+@pytest.mark.parametrize("H", [513, 700, 1001, 2046, 4097, 8185, 32767])
+@pytest.mark.parametrize("rdt,gdt", [(BF16, F32), (F32, BF16)])
+def test_rows_of_any_start_into_contiguous_outputs(H, rdt, gdt):
+    """Inputs with gaps of any size, outputs without: rows start anywhere; gamma one element off a boundary."""
+    gen = torch.Generator().manual_seed(H)
+    for T, pad in ((1, 0), (19, 0), (19, 1), (9, 5), (300 if H < 5000 else 12, 13)):
+        _, x = strided(T, H, pad, BF16, gen)
+        _, r = strided(T, H, pad + 2, rdt, gen, 3.0)
+        g = torch.ones((H + 1,), dtype=gdt, device="cuda")[1:]
+        g.copy_((1 + 0.3 * torch.randn((H,), generator=gen)).to(gdt))
+        room = lambda dt: torch.full((T * H + 16,), 7.0, device="cuda").to(dt)                      # noqa: E731
+        sb, ob, cb = room(rdt), room(BF16), room(torch.float8_e4m3fn)
+        total, out, codes = (t[:T * H].view(T, H) for t in (sb, ob, cb))
+        scale = torch.zeros((T,), device="cuda")
+        call(x, r, g, total, out, codes, scale)
+        check(x, r, g, total, out, codes, scale)
+        call(x, None, g, None, out, None, None)
+        check(x, None, g, None, out, None, None)
+        for b in (sb, ob, cb):                                  # nothing behind the last row
+            assert (b[T * H:].float() == 7.0).all()
+
+
+@pytest.mark.parametrize("H", [1001, 7001])
+@pytest.mark.parametrize("rdt", [BF16, F32])
+def test_in_place_rows_of_any_start(H, rdt):
+    gen = torch.Generator().manual_seed(9)
+    for T in (7, 400):
+        x = torch.randn((T, H), generator=gen).to(BF16).cuda()
+        r = torch.randn((T, H), generator=gen).to(rdt).cuda()
+        g = torch.ones((H,), device="cuda")
+        x0, r0 = x.clone(), r.clone()
+        call(x, r, g, r, x, None, None)
+        check(x0, r0, g, r, x, None, None)
