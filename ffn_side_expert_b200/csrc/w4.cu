@@ -134,7 +134,8 @@ struct UnitTables {
 };
 
 // Rows and unit bases of every expert from counts: negative counts are flagged and taken as 0,
-// rows past n_rows are flagged and cut off.  units_of(rows): an expert's units.
+// rows past n_rows are flagged and cut off.  units_of(rows): an expert's units, asked of all threads after a
+// barrier.
 template <typename F>
 __device__ __forceinline__ void build_tables(const W4Args& a, F units_of, UnitTables& tb, int* wsum) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -155,7 +156,7 @@ __device__ __forceinline__ void build_tables(const W4Args& a, F units_of, UnitTa
   const int first = min(incl - c, a.n_rows);
   const int rows = min(c, a.n_rows - first);
   if (bad && blockIdx.x == 0) atomicOr(a.err, kErrBadOffsets);
-  const int units = tid < a.E ? units_of(rows) : 0;
+  const int units = units_of(rows);  // by all threads; 0 rows past the last expert
   int uincl = warp_incl_scan(units, lane);
   __syncthreads();
   if (lane == 31) wsum[warp] = uincl;
@@ -339,8 +340,8 @@ int launch_w4(const afd_ffn_w4& w, int E, const void* x, const int32_t* counts, 
   const uint64_t row_bytes = w.K / 2, rows = static_cast<uint64_t>(E) * w.N;
   cudaError_t e = cudaSuccess;
   // A second kernel takes about 5 us to start, in which 32 MB of codes stream: smaller weights go to one
-  // kernel (16 rows on each of 8 experts of 256 x 512: 26 us with two a product, 17 us with one).
-  const bool small = static_cast<long long>(E) * w.N * (w.K / 2) <= 32 << 20;
+  // kernel, unless K is long, which units of few rows split better (16 rows on each of 8 experts of 256 x 512: 26 us with two a product, 17 us with one).
+  const bool small = static_cast<long long>(E) * w.N * (w.K / 2) <= 32 << 20 && w.K <= 1024;
   a.above = small ? 0 : kNarrowN;
   if (!more || (counts && !small)) {
     const bool wide = w.group % 128 == 0;  // steps of 256 inputs

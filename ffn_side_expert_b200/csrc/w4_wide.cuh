@@ -51,19 +51,27 @@ __device__ __forceinline__ void group_barrier(int id, int threads) {
   asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
 }
 
-// Warpgroups that share a unit, each with its own slices: the split of the least cost, where a team
-// takes ceil(units / teams) units of ceil(slices / split) steps and about 1.5 more for the join.
-__device__ __forceinline__ int choose_wide_split(unsigned units, unsigned slices, unsigned ctas) {
-  const int lane = threadIdx.x & 31, log = 2 - lane;  // a lane for each candidate
-  static_assert(kWgs == 4, "splits of 4, 2 and 1");
+// Columns of a unit and warpgroups that share one, each with its own slices.
+struct WideShape {
+  int cols, split;
+};
+
+// The shape of the least cost: a team takes ceil(units / teams) units of ceil(slices / split) steps and about
+// 1.5 more for the join; a step of 32 columns takes 1.2 and one of 64 twice the time of one of 16.
+// tiles: token tiles of all experts at 16, 32 and 64 columns.
+__device__ __forceinline__ WideShape choose_wide(const int* tiles, unsigned blocks, unsigned slices, unsigned ctas) {
+  const int lane = threadIdx.x & 31, log = lane % 3, size = lane / 3;  // a lane for each candidate
+  static_assert(kWgs == 4, "splits of 1, 2 and 4");
   unsigned cost = 0xffffffffu;
-  if (lane < 3) {
-    const unsigned teams = ctas * (kWgs >> log);
+  if (lane < 9) {
+    const unsigned teams = ctas * (kWgs >> log), units = tiles[size] * blocks;
+    const float step = size == 0 ? 10.f : size == 1 ? 12.f : 20.f;
     const float c = static_cast<float>((units + teams - 1) / teams) *
-                    static_cast<float>(((slices + (1u << log) - 1) >> log) * 10u + 15u);
+                    (static_cast<float>((slices + (1u << log) - 1) >> log) * step + 15.f);
     cost = (__float_as_uint(c) & ~31u) | lane;
   }
-  return kWgs >> (__reduce_min_sync(0xffffffffu, cost) & 31);
+  const int best = __reduce_min_sync(0xffffffffu, cost) & 31;
+  return WideShape{16 << best / 3, 1 << best % 3};
 }
 
 struct WideUnit {
@@ -71,15 +79,14 @@ struct WideUnit {
 };
 
 template <int MODE>
-__device__ __forceinline__ WideUnit wide_unit_at(int u, int* e, const UnitTables& tb) {
-  constexpr int kTokens = kWideCols / (MODE == kDown ? 2 : 1);
+__device__ __forceinline__ WideUnit wide_unit_at(int u, int* e, int tokens, const UnitTables& tb) {
   while (u >= tb.unit_base[*e + 1]) ++*e;
   WideUnit r;
   r.e = *e;
-  const int rows = tb.rows[r.e], tiles = (rows + kTokens - 1) / kTokens;
+  const int rows = tb.rows[r.e], tiles = (rows + tokens - 1) / tokens;
   const int at = u - tb.unit_base[r.e], block = at / tiles, tile = at - block * tiles;
-  r.first = tb.first[r.e] + tile * kTokens;
-  r.m = min(kTokens, rows - tile * kTokens);
+  r.first = tb.first[r.e] + tile * tokens;
+  r.m = min(tokens, rows - tile * tokens);
   r.row0 = block * (MODE == kGateUp ? kWideRows / 2 : kWideRows);
   return r;
 }
@@ -88,7 +95,7 @@ __device__ __forceinline__ WideUnit wide_unit_at(int u, int* e, const UnitTables
 template <int MODE, int PARTS>
 __global__ void __launch_bounds__(kWideThreads, 1)
 w4_wide_kernel(const __grid_constant__ CUtensorMap codes, const W4Args a) {
-  constexpr int kPlanes = MODE == kDown ? 2 : 1, kTokens = kWideCols / kPlanes;
+  constexpr int kPlanes = MODE == kDown ? 2 : 1;
   constexpr int kOut = MODE == kGateUp ? kWideRows / 2 : kWideRows;
   extern __shared__ uint8_t smem_raw[];
   __shared__ UnitTables tb;
@@ -105,7 +112,23 @@ w4_wide_kernel(const __grid_constant__ CUtensorMap codes, const W4Args a) {
 
   const int outs = MODE == kGateUp ? a.N / 2 : a.N;
   const int blocks = (outs + kOut - 1) / kOut;
-  build_tables(a, [&](int rows) { return rows * kPlanes > a.above ? (rows + kTokens - 1) / kTokens * blocks : 0; }, tb, wsum);
+  __shared__ int tiles[3];
+  if (tid < 3) tiles[tid] = 0;
+  const int slices = (a.K + kSliceK - 1) / kSliceK;
+  WideShape shape{};
+  build_tables(a, [&](int rows) {
+    if (rows * kPlanes <= a.above) rows = 0;
+#pragma unroll
+    for (int i = 0; i < 3; ++i) {
+      const int n = __reduce_add_sync(0xffffffffu, (rows * kPlanes + (16 << i) - 1) >> (4 + i));
+      if ((tid & 31) == 0 && n) atomicAdd(&tiles[i], n);
+    }
+    __syncthreads();
+    shape = choose_wide(tiles, blocks, slices, gridDim.x);
+    const int tokens = shape.cols / kPlanes;
+    return (rows + tokens - 1) / tokens * blocks;
+  }, tb, wsum);
+  const int tile = shape.cols / kPlanes;
   const int total = tb.unit_base[a.E];
   if (total == 0) {
     wait_dependency();  // what follows may rely on the kernel before this one
@@ -138,8 +161,7 @@ w4_wide_kernel(const __grid_constant__ CUtensorMap codes, const W4Args a) {
   const uint32_t tm_a = tmem + wg * 64, tm_d = tmem + 256 + wg * 64;
 
   const int KG = a.K / a.G, cps = a.scale_f32 ? 4 : 2;
-  const int slices = (a.K + kSliceK - 1) / kSliceK;
-  const int split = choose_wide_split(total, slices, gridDim.x);
+  const int split = shape.split;
   const int sub = wg & (split - 1), team = wg / split;
   const int per = (slices + split - 1) / split;  // a group's consecutive slices
   const int steps = max(0, min(per, slices - sub * per));
@@ -160,7 +182,7 @@ w4_wide_kernel(const __grid_constant__ CUtensorMap codes, const W4Args a) {
   auto load_step = [&]() {
     if (lu >= total || *abort) return;
     if (ls == 0) {
-      const WideUnit un = wide_unit_at<MODE>(lu, &le, tb);
+      const WideUnit un = wide_unit_at<MODE>(lu, &le, tile, tb);
       lrow = un.e * a.N + un.row0;
       lx = sub * per * (kSliceK / 2);
     }
@@ -190,7 +212,7 @@ w4_wide_kernel(const __grid_constant__ CUtensorMap codes, const W4Args a) {
   int pe = 0;
   auto prefetch_scales = [&](int u) {
     if (u >= total) return;
-    const size_t at = scale_row(wide_unit_at<MODE>(u, &pe, tb));
+    const size_t at = scale_row(wide_unit_at<MODE>(u, &pe, tile, tb));
     const uint8_t* sp = static_cast<const uint8_t*>(a.scale) + at * cps;
     for (int o = sub * 32; o < KG * cps; o += split * 32) prefetch_l2(sp + o);
     if (a.zero)
@@ -202,7 +224,7 @@ w4_wide_kernel(const __grid_constant__ CUtensorMap codes, const W4Args a) {
   int it = 0, ce = 0;
   uint32_t mma_phase = 0;
   for (int u = u0; u < total; u += teams) {
-    const WideUnit un = wide_unit_at<MODE>(u, &ce, tb);
+    const WideUnit un = wide_unit_at<MODE>(u, &ce, tile, tb);
     const int cols = un.m * kPlanes;
     const size_t srow = scale_row(un);
     prefetch_scales(u + teams);
