@@ -43,19 +43,21 @@ struct NarrowShape {
 };
 
 // The shape of the least cost: a team takes ceil(units / teams) units of ceil(steps / split) steps and
-// about half of one more for the join.  R rows leave R / 8 columns.  A lane works out each candidate: one after
-// another the divisions took 2 us of a kernel's start.
-__device__ __forceinline__ NarrowShape choose_narrow(int experts, int outs, int log_pair, int slices, int ctas, int wgs,
-                                                     int cols) {
+// about one more for its first loads and the join.  Fewer rows are more scales, tokens and TMA boxes a step: counted
+// as equal, 18 experts of 3840 x 1024 took units of 64 rows and 59 us, where 128 rows take 50.  R rows leave R / 8 columns; tiles: token tiles of all experts at 16,
+// 8 and 4 columns.  A lane works out each candidate: one after another the divisions took 2 us of a kernel's
+// start.
+__device__ __forceinline__ NarrowShape choose_narrow(const int* tiles, int outs, int log_pair, int slices, int ctas, int wgs) {
   const int lane = threadIdx.x & 31, lr = 7 - (lane >> 1), split = lane & 1 ? wgs : 1;
   unsigned cost = 0xffffffffu;
-  if (lane < 6 && cols <= (1 << lr) / 8) {
-    const unsigned units = experts * (static_cast<unsigned>(outs + (1 << (lr - log_pair)) - 1) >> (lr - log_pair));
+  if (lane < 6) {
+    const unsigned units = tiles[lane >> 1] * (static_cast<unsigned>(outs + (1 << (lr - log_pair)) - 1) >> (lr - log_pair));
     const unsigned steps = static_cast<unsigned>(slices + (128 >> lr) - 1) >> (7 - lr);
     const unsigned teams = ctas * (split == 1 ? wgs : 1);
     // up to 2^24 in floats, which is enough for a choice, with room for the candidate below it
+    const float step = lane < 2 ? 10.f : lane < 4 ? 14.f : 18.f;
     const float c = static_cast<float>((units + teams - 1) / teams) *
-                    static_cast<float>((split == 1 ? steps : (steps + wgs - 1) / static_cast<unsigned>(wgs)) * 10u + 6u);
+                    (static_cast<float>(split == 1 ? steps : (steps + wgs - 1) / static_cast<unsigned>(wgs)) * step + 8.f);
     cost = (__float_as_uint(c) & ~31u) | lane;
   }
   const int best = __reduce_min_sync(0xffffffffu, cost) & 31;
@@ -101,10 +103,10 @@ w4_narrow_kernel(const __grid_constant__ NarrowMaps codes, const W4Args a) {
   constexpr int kPartK = S / PARTS, kPer = S / 16 / PARTS;  // inputs and K16 steps of a part
   static_assert(PARTS * N <= L::kAccs, "every part has an accumulator");
   extern __shared__ uint8_t smem_raw[];
-  __shared__ UnitTables tb;                          // unit_base: rank of an expert among those with units
-  __shared__ int experts[kW4MaxExperts];             // by rank
+  __shared__ UnitTables tb;                          // unit_base: token tiles of the experts before
+  __shared__ uint16_t tile_of[4 * kW4MaxExperts];    // of a token tile: its expert, and its number there * 256
   __shared__ int wsum[kThreads / 32];
-  __shared__ int most;                               // columns of an expert
+  __shared__ int tiles[3];
   __shared__ __align__(8) uint64_t bars[kWgs * (kStages + 1)];
   __shared__ uint32_t tmem_slot;
   __shared__ int abort_flag;
@@ -116,17 +118,28 @@ w4_narrow_kernel(const __grid_constant__ NarrowMaps codes, const W4Args a) {
   volatile int* abort = &abort_flag;
 
   const int outs = MODE == kGateUp ? a.N / 2 : a.N;
-  if (tid == 0) most = 0;
-  build_tables(a, [&](int rows) { return rows > 0 && rows * kPlanes <= kNarrowN ? 1 : 0; }, tb, wsum);
-  const int n_experts = tb.unit_base[a.E];
-  if (n_experts == 0) {
+  if (tid < 3) tiles[tid] = 0;
+  const int slices = (a.K + S - 1) / S;
+  NarrowShape shape{};
+  build_tables(a, [&](int rows) {
+    if (rows * kPlanes > N) rows = 0;
+#pragma unroll
+    for (int i = 0; i < 3; ++i) {
+      const int n = __reduce_add_sync(0xffffffffu, (rows * kPlanes + (16 >> i) - 1) >> (4 - i));
+      if ((tid & 31) == 0 && n) atomicAdd(&tiles[i], n);
+    }
+    __syncthreads();
+    shape = choose_narrow(tiles, outs, kLogPair, slices, gridDim.x, kWgs);
+    return (rows * kPlanes + (1 << shape.log_rows) / 8 - 1) >> (shape.log_rows - 3);
+  }, tb, wsum);
+  const int n_tiles = tb.unit_base[a.E];
+  if (n_tiles == 0) {
     wait_dependency();  // what follows may rely on the kernel before this one
     return;
   }
-  if (tid < a.E && tb.unit_base[tid + 1] > tb.unit_base[tid]) {
-    experts[tb.unit_base[tid]] = tid;
-    atomicMax(&most, tb.rows[tid] * kPlanes);
-  }
+  if (tid < a.E)
+    for (int i = tb.unit_base[tid]; i < tb.unit_base[tid + 1]; ++i)
+      tile_of[i] = static_cast<uint16_t>(tid | (i - tb.unit_base[tid]) << 8);
   const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;
   uint8_t* const gbase = smem_raw + (base - smem_u32(smem_raw));
   constexpr int kRingOff = kWgs * L::kTokens, kWindowOff = kRingOff + kWgs * kStages * L::kStep;
@@ -154,8 +167,6 @@ w4_narrow_kernel(const __grid_constant__ NarrowMaps codes, const W4Args a) {
   constexpr uint32_t idesc = idesc_mn(128, N, false);
 
   const int KG = a.K / a.G, cps = a.scale_f32 ? 4 : 2;
-  const int slices = (a.K + S - 1) / S;
-  const NarrowShape shape = choose_narrow(n_experts, outs, kLogPair, slices, gridDim.x, kWgs, most);
   const int split = shape.split;
   int it = 0, issued = 0;                            // steps of this group: taken, and under way
 
@@ -168,7 +179,7 @@ w4_narrow_kernel(const __grid_constant__ NarrowMaps codes, const W4Args a) {
     constexpr int kStack = 128 >> LR;                  // slices of a step
     constexpr int kOutRows = R >> kLogPair;            // outputs of a unit
     const int blocks = (outs + kOutRows - 1) / kOutRows;
-    const int total = n_experts * blocks;
+    const int total = n_tiles * blocks;
     const int ksteps = (slices + kStack - 1) / kStack, per = (ksteps + split - 1) / split;
     const int sub = split == 1 ? 0 : wg, team = split == 1 ? wg : 0;
     const int steps = max(0, min(per, ksteps - sub * per));
@@ -181,12 +192,12 @@ w4_narrow_kernel(const __grid_constant__ NarrowMaps codes, const W4Args a) {
       int e, first, m, row0;  // expert, first token row, tokens, first output
     };
     auto unit_of = [&](int u) {
-      const int rank = u / blocks;
+      const int at = u / blocks, tile = tile_of[at];
       At t;
-      t.e = experts[rank];
-      t.first = tb.first[t.e];
-      t.m = tb.rows[t.e];
-      t.row0 = (u - rank * blocks) * kOutRows;
+      t.e = tile & 255;
+      t.first = tb.first[t.e] + (tile >> 8) * (C / kPlanes);
+      t.m = min(C / kPlanes, tb.rows[t.e] - (tile >> 8) * (C / kPlanes));
+      t.row0 = (u - at * blocks) * kOutRows;
       return t;
     };
 
