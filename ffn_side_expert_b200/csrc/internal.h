@@ -8,6 +8,24 @@
 
 namespace afd {
 
+// Launch a kernel that may start while the stream's kernel before it ends (ptx.cuh: wait_dependency): about a
+// microsecond less between two small kernels.
+template <typename... Args>
+cudaError_t launch_dependent(void (*kernel)(Args...), unsigned grid, unsigned threads, size_t smem, cudaStream_t s,
+                             const Args&... args) {
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr{};
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
 // Record the error of a call without a handle (afd_ffn_last_cuda_error(NULL)); AFD_ERR_CUDA.
 int rows_cuda_fail(cudaError_t e);
 

@@ -15,6 +15,7 @@
 #include "afd_ffn.h"
 #include "common.cuh"
 #include "internal.h"
+#include "ptx.cuh"
 
 namespace afd {
 namespace {
@@ -94,6 +95,8 @@ __device__ __forceinline__ float divide(float a, float b, float r) {
 template <int V, int N, int MAXT, int MINB, typename RT, typename GT>
 __global__ void __launch_bounds__(MAXT, MINB)
 add_rmsnorm_kernel(const NormArgs a) {
+  launch_dependents();
+  wait_dependency();
   __shared__ float red_sum[32];
   __shared__ unsigned red_top[32];
   const long long t = blockIdx.x;
@@ -233,6 +236,8 @@ __device__ __forceinline__ void load_shifted(const T* p, const T* begin, const T
 template <int N, int MAXT, int MINB, typename RT, typename GT>
 __global__ void __launch_bounds__(MAXT, MINB)
 add_rmsnorm_shifted_kernel(const NormArgs a) {
+  launch_dependents();
+  wait_dependency();
   __shared__ float red_sum[32];
   __shared__ unsigned red_top[32];
   const long long t = blockIdx.x, flat = t * a.H;
@@ -337,7 +342,7 @@ add_rmsnorm_shifted_kernel(const NormArgs a) {
 template <int V, int N, int MAXT, int MINB, typename RT, typename GT>
 void launch_norm_kernel(const NormArgs& a, int T, cudaStream_t s) {
   const int threads = (a.H / V + N * 32 - 1) / (N * 32) * 32;
-  add_rmsnorm_kernel<V, N, MAXT, MINB, RT, GT><<<T, threads, 0, s>>>(a);
+  launch_dependent(add_rmsnorm_kernel<V, N, MAXT, MINB, RT, GT>, T, threads, 0, s, a);
 }
 
 // Pieces per thread and CTAs per SM.  Few rows: one piece, the shortest way through a row.  Rows that
@@ -373,9 +378,9 @@ template <typename RT, typename GT>
 void launch_shifted(const NormArgs& a, int T, cudaStream_t s) {
   const int pieces = (a.H + 14) / 8;  // at most
   const int per = pieces <= 256 ? 1 : pieces <= 1024 ? 2 : 5, threads = (pieces + per * 32 - 1) / (per * 32) * 32;
-  if (per == 1) add_rmsnorm_shifted_kernel<1, 256, 4, RT, GT><<<T, threads, 0, s>>>(a);
-  else if (per == 2) add_rmsnorm_shifted_kernel<2, 512, 4, RT, GT><<<T, threads, 0, s>>>(a);
-  else add_rmsnorm_shifted_kernel<5, 1024, 1, RT, GT><<<T, threads, 0, s>>>(a);
+  if (per == 1) launch_dependent(add_rmsnorm_shifted_kernel<1, 256, 4, RT, GT>, T, threads, 0, s, a);
+  else if (per == 2) launch_dependent(add_rmsnorm_shifted_kernel<2, 512, 4, RT, GT>, T, threads, 0, s, a);
+  else launch_dependent(add_rmsnorm_shifted_kernel<5, 1024, 1, RT, GT>, T, threads, 0, s, a);
 }
 
 // How rows move: 16-byte pieces, shifted pieces, single elements.

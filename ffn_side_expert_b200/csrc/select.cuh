@@ -29,6 +29,8 @@
 #include <cfloat>
 
 #include "common.cuh"
+#include "internal.h"
+#include "ptx.cuh"
 
 namespace afd {
 
@@ -220,6 +222,8 @@ constexpr int kSelectWarps = 4;  // tokens per CTA
 template <typename LT>
 __global__ void __launch_bounds__(kSelectWarps * 32)
 select_experts_kernel(const SelectArgs a) {
+  launch_dependents();
+  wait_dependency();
   __shared__ float s_logit[kSelectWarps][256];
   __shared__ double s_choice[kSelectWarps][256];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -424,7 +428,7 @@ select_experts_kernel(const SelectArgs a) {
 
 template <typename LT>
 inline void launch_select_experts(const SelectArgs& a, cudaStream_t s) {
-  select_experts_kernel<LT><<<(a.T + kSelectWarps - 1) / kSelectWarps, kSelectWarps * 32, 0, s>>>(a);
+  launch_dependent(select_experts_kernel<LT>, (a.T + kSelectWarps - 1) / kSelectWarps, kSelectWarps * 32, 0, s, a);
 }
 
 }  // namespace afd

@@ -10,11 +10,16 @@
 // is scaled in fp32, the factor 4 comes back at the end.  The SwiGLU rows are kept as two bf16
 // terms (hi + lo, 2^-17 relative), which are two columns of the down product.
 //
+// Both products run on the 5th-generation tensor cores with the unpacked weights as the A operand in TMEM:
+// experts with up to 16 columns (tokens, or planes of tokens) in w4_narrow.cuh, the others in
+// w4_wide.cuh.  A warp's mma.sync on codes unpacked in registers, tried first, was bound by the same
+// unpacking with more instructions around it (one token's eight experts of H = 7168, I = 2048: 66 us
+// against 60; 128 rows on 64 experts of 4096 x 1024: 143 against 101).
+//
 // What bounds it.  At the HBM rate an SM gets 46 codes a clock, and its integer pipe does 64 lane
 // operations; so the unpacking decides.  A word of eight codes takes nine instructions, five of
 // them integer: one shift, four masks and four bf16x2 FMAs that take the zero point off
-// (unpack_word).  Weights come through a cp.async ring per warp, straight from HBM; the inputs,
-// few, from L1 and L2.
+// (unpack_word).
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -32,15 +37,7 @@ namespace {
 
 constexpr int kW4MaxExperts = 256;
 constexpr int kW4MaxRows = 1 << 22;
-constexpr int kWarps = 8, kThreads = kWarps * 32;
-constexpr int kSliceK = 128;       // inputs a warp takes in one step
-constexpr int kBlockRows = 16;     // weight rows of a block (SwiGLU: 8 gate rows and their 8 up rows); a unit is one or two
-constexpr int kTileBytes = 2 * kBlockRows * kSliceK / 2;
-constexpr int kCols = 8;           // columns of a unit: 8 tokens, or 4 of two planes
-constexpr int kRedPitch = 2 * kBlockRows + 4;
-constexpr int kInputBytes = kCols * kSliceK * 2;
-constexpr int kStageBytes = kTileBytes + kInputBytes;
-constexpr int kStages = 3;         // two steps ahead: 64 KB in flight on an SM, and what fits it twice
+constexpr int kSliceK = 128;       // inputs of a slice of K
 
 struct W4Args {
   const uint8_t* codes;
@@ -53,6 +50,7 @@ struct W4Args {
   unsigned group_inv;       // ceil(2^32 / (G / 32)), 0 for groups of 32
   int glog;                 // log2 G, where windows says so
   int windows;              // groups of 2^i, rows of scales (and zero points) that whole 16-byte pieces cover
+  int first;                // this kernel is the call's first: its inputs may come from the kernel before it
   int above;                // w4_wide.cuh: the experts with more columns than this
   int* err;
 };
@@ -79,18 +77,6 @@ __device__ __forceinline__ void prefetch_l2(const void* p) { asm volatile("prefe
 __device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
 __device__ __forceinline__ void cp_async_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
-// This kernel's dependents may start; wait for the kernel this one depends on (nothing outside a
-// programmatic launch).
-__device__ __forceinline__ void launch_dependents() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
-__device__ __forceinline__ void wait_dependency() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
-
-// D (16 x 8, fp32) = A (16 x 16, bf16) B (16 x 8, bf16) + C
-__device__ __forceinline__ void mma_bf16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
-                                         uint32_t b1, const float (&c)[4]) {
-  asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%10, %11, %12, %13};"
-      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
-      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(c[0]), "f"(c[1]), "f"(c[2]), "f"(c[3]));
-}
 
 __device__ __forceinline__ uint32_t fma_bf16x2(uint32_t a, uint32_t b, uint32_t c) {
   uint32_t d;
@@ -171,35 +157,6 @@ __device__ __forceinline__ void build_tables(const W4Args& a, F units_of, UnitTa
   __syncthreads();
 }
 
-// One unit: an expert with its m tokens from row `first`, and mt blocks of its weight rows from
-// output row0 on, over the whole of K.
-struct Unit {
-  int e, first, m, row0, mt;
-};
-
-// The unit at block b of a team's blocks, which end at `end`.
-template <bool SWIGLU>
-__device__ __forceinline__ Unit unit_at(int b, int end, int* e, const UnitTables& tb) {
-  while (b >= tb.unit_base[*e + 1]) ++*e;
-  Unit r;
-  r.e = *e;
-  r.first = tb.first[r.e];
-  r.m = tb.rows[r.e];
-  r.row0 = (b - tb.unit_base[r.e]) * (SWIGLU ? kBlockRows / 2 : kBlockRows);
-  r.mt = b + 1 < min(end, tb.unit_base[r.e + 1]) ? 2 : 1;
-  return r;
-}
-
-// Weight row (inside the expert) of row i * 8 + g of a unit; rows past the end repeat the last one.
-template <bool SWIGLU>
-__device__ __forceinline__ int weight_row(const W4Args& a, int row0, int i, int g) {
-  if (SWIGLU) {
-    const int half = a.N / 2;
-    return ((i & 1) ? half : 0) + min(row0 + (i >> 1) * 8 + g, half - 1);
-  }
-  return min(row0 + i * 8 + g, a.N - 1);
-}
-
 // Group of the 32 inputs kq: kq / (G / 32).
 __device__ __forceinline__ int group_of(const W4Args& a, int kq) {
   return a.group_inv ? static_cast<int>(__umulhi(static_cast<unsigned>(kq), a.group_inv)) : kq;
@@ -267,14 +224,12 @@ int check_w4_pointers(const afd_ffn_w4* w) {
   return AFD_OK;
 }
 
-constexpr int kRingBytes = kWarps * kStages * kStageBytes;
 constexpr int kMaxDevices = 64;
 
-// A kernel's launch on the current device; at most one of the stream's kernels may still run when it
-// starts (programmatic), which it waits for before it reads what that one writes.
+// A kernel's launch on the current device, as the dependent of the stream's last one.
 template <typename... Args>
-cudaError_t launch_on_device(void (*kernel)(Args...), std::atomic<int>* sm_count, int ctas_per_sm, int threads, int smem,
-                             bool programmatic, cudaStream_t s, const Args&... args) {
+cudaError_t launch_on_device(void (*kernel)(Args...), std::atomic<int>* sm_count, int threads, int smem, cudaStream_t s,
+                             const Args&... args) {
   // per device and kernel, once: the SM count, and leave for the shared memory
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
@@ -286,30 +241,19 @@ cudaError_t launch_on_device(void (*kernel)(Args...), std::atomic<int>* sm_count
     if (e != cudaSuccess) return e;
     if (dev < kMaxDevices) sm_count[dev].store(sms, std::memory_order_relaxed);
   }
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(ctas_per_sm * sms);
-  cfg.blockDim = dim3(threads);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = s;
-  cudaLaunchAttribute attr{};
-  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr.val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = &attr;
-  cfg.numAttrs = programmatic ? 1 : 0;
-  return cudaLaunchKernelEx(&cfg, kernel, args...);
+  return launch_dependent(kernel, sms, threads, smem, s, args...);
 }
 
 template <int MODE, int PARTS>
-cudaError_t launch_wide(const CUtensorMap& codes, const W4Args& a, bool programmatic, cudaStream_t s) {
+cudaError_t launch_wide(const CUtensorMap& codes, const W4Args& a, cudaStream_t s) {
   static std::atomic<int> sm_count[kMaxDevices];
-  return launch_on_device(w4_wide_kernel<MODE, PARTS>, sm_count, 1, kWideThreads, kWideSmem, programmatic, s, codes, a);
+  return launch_on_device(w4_wide_kernel<MODE, PARTS>, sm_count, kWideThreads, kWideSmem, s, codes, a);
 }
 
 template <int MODE, int PARTS, int S>
-cudaError_t launch_narrow(const NarrowMaps& codes, const W4Args& a, bool programmatic, cudaStream_t s) {
+cudaError_t launch_narrow(const NarrowMaps& codes, const W4Args& a, cudaStream_t s) {
   static std::atomic<int> sm_count[kMaxDevices];
-  return launch_on_device(w4_narrow_kernel<MODE, PARTS, S>, sm_count, 1, Narrow<S>::kThreads, Narrow<S>::kSmem, programmatic,
-                          s, codes, a);
+  return launch_on_device(w4_narrow_kernel<MODE, PARTS, S>, sm_count, Narrow<S>::kThreads, Narrow<S>::kSmem, s, codes, a);
 }
 
 // One product: the experts with few rows, then those with more.  Only a call that can have such
@@ -336,6 +280,7 @@ int launch_w4(const afd_ffn_w4& w, int E, const void* x, const int32_t* counts, 
               (reinterpret_cast<uintptr_t>(w.zero) & (piece - 1)) == 0;
   while (a.glog < 31 && 1 << (a.glog + 1) <= w.group) ++a.glog;
   a.err = err;
+  a.first = !after;
   const bool more = static_cast<long long>(n_rows) * kPlanes > kNarrowN;
   const uint64_t row_bytes = w.K / 2, rows = static_cast<uint64_t>(E) * w.N;
   cudaError_t e = cudaSuccess;
@@ -348,18 +293,18 @@ int launch_w4(const afd_ffn_w4& w, int E, const void* x, const int32_t* counts, 
     NarrowMaps maps;
     for (int i = 0; i < 3; ++i)
       if (!encode_byte_rows(&maps.map[i], w.codes, row_bytes, rows, wide ? 128 : 64, 64 >> i)) return AFD_ERR_NO_DEVICE;
-    e = w.group % 256 == 0  ? launch_narrow<MODE, 1, 256>(maps, a, after, s)
-        : wide              ? launch_narrow<MODE, 2, 256>(maps, a, after, s)
-        : w.group % 64 == 0 ? launch_narrow<MODE, 2, 128>(maps, a, after, s)
-                            : launch_narrow<MODE, 4, 128>(maps, a, after, s);
-    after = true;
+    e = w.group % 256 == 0  ? launch_narrow<MODE, 1, 256>(maps, a, s)
+        : wide              ? launch_narrow<MODE, 2, 256>(maps, a, s)
+        : w.group % 64 == 0 ? launch_narrow<MODE, 2, 128>(maps, a, s)
+                            : launch_narrow<MODE, 4, 128>(maps, a, s);
+    a.first = 0;
   }
   if (more && e == cudaSuccess) {
     CUtensorMap map;
     if (!encode_byte_rows(&map, w.codes, row_bytes, rows, kSliceK / 2, kWideRows / 2)) return AFD_ERR_NO_DEVICE;
-    e = w.group % 128 == 0  ? launch_wide<MODE, 1>(map, a, after, s)
-        : w.group % 64 == 0 ? launch_wide<MODE, 2>(map, a, after, s)
-                            : launch_wide<MODE, 4>(map, a, after, s);
+    e = w.group % 128 == 0  ? launch_wide<MODE, 1>(map, a, s)
+        : w.group % 64 == 0 ? launch_wide<MODE, 2>(map, a, s)
+                            : launch_wide<MODE, 4>(map, a, s);
   }
   return e == cudaSuccess ? AFD_OK : rows_cuda_fail(e);
 }

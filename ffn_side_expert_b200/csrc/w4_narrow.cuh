@@ -117,6 +117,7 @@ w4_narrow_kernel(const __grid_constant__ NarrowMaps codes, const W4Args a) {
   const int wg = warp >> 2, r = tid & 127;           // warpgroup; TMEM lane
   volatile int* abort = &abort_flag;
 
+  if (a.first) wait_dependency();
   const int outs = MODE == kGateUp ? a.N / 2 : a.N;
   if (tid < 3) tiles[tid] = 0;
   const int slices = (a.K + S - 1) / S;

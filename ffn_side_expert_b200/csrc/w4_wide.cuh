@@ -110,6 +110,7 @@ w4_wide_kernel(const __grid_constant__ CUtensorMap codes, const W4Args a) {
   const int wg = warp >> 2, r = tid & 127;  // warpgroup; row of the unit, which is the TMEM lane
   volatile int* abort = &abort_flag;
 
+  if (a.first) wait_dependency();
   const int outs = MODE == kGateUp ? a.N / 2 : a.N;
   const int blocks = (outs + kOut - 1) / kOut;
   __shared__ int tiles[3];
