@@ -209,12 +209,12 @@ int check_w4(const afd_ffn_w4* w, int32_t E) {
   return AFD_OK;
 }
 
-// Units are counted in 32 bits: blocks of at least 8 outputs of every expert, and tiles of at least 32
-// tokens by 64 outputs.
+// Units are counted in 32 bits: blocks of at least 16 outputs for up to four token tiles of every expert, and
+// tiles of at least 8 tokens by 64 outputs.
 bool units_fit(int n_rows, int E, int outs) {
-  const long long few = static_cast<long long>(E) * (outs / 8 + 1);
-  const long long wide = (static_cast<long long>(n_rows) / 32 + E) * (outs / 64 + 1);
-  return few < (1LL << 31) - 65536 && wide < (1LL << 31) - 65536;
+  const long long narrow = 4LL * E * (outs / 16 + 1);
+  const long long wide = (static_cast<long long>(n_rows) / 8 + E) * (outs / 64 + 1);
+  return narrow < (1LL << 31) - 65536 && wide < (1LL << 31) - 65536;
 }
 
 int check_w4_pointers(const afd_ffn_w4* w) {

@@ -329,9 +329,11 @@ int afd_ffn_combine_rows_bf16(const void *Y, const void *Ys, const float *topk_w
 
 /* ---- 4-bit experts ------------------------------------------------------------------
  * Rows grouped by expert times weights in 4 bits with one scale per group of `group` consecutive
- * input elements: W[n][k] = (q[n][k] - z[n][k / group]) * scale[n][k / group].  Written for the
- * few rows an expert gets in a decode micro-batch, where the time is that of streaming the
- * weights (a quarter of bf16's bytes); it is right, though not fast, for many rows. */
+ * input elements: W[n][k] = (q[n][k] - z[n][k / group]) * scale[n][k / group].  For the few rows an
+ * expert gets in a decode micro-batch, where the weights, a quarter of bf16's bytes, are what
+ * moves; for many rows each 64 of an expert unpack its weights once more.  Groups of 128 or more
+ * are the fast ones, and rows of scales (K / group of them) that are whole 16-byte pieces from a
+ * 16-byte boundary on. */
 typedef struct {              /* DEVICE pointers, borrowed, never written                     */
     const void    *codes;     /* [E][N][K/2] bytes, 16-byte aligned: element k = 2i of a row in
                                  the low four bits of byte i, k = 2i + 1 in the high four      */
@@ -346,9 +348,11 @@ typedef struct {              /* DEVICE pointers, borrowed, never written       
 /* y[r] = x[r] W_e^T for rows grouped by expert: x [n_rows][K] bf16, counts [E] (device; rows of
  * expert 0 first, then expert 1, ...) or NULL with E == 1 (one matrix for every row) ->
  * y [n_rows][N] bf16 or fp32 (y_dtype), summed in fp32 and rounded once.  x, y 16-byte aligned,
- * y apart from every input.  E <= 256, n_rows <= 2^22.  Rows behind the last expert's stay as they were.  A
- * negative count is taken as 0 and rows past n_rows are cut off; both are flagged
- * (afd_ffn_rows_error).  Asynchronous on `stream`; capturable after one call on the device. */
+ * y apart from every input.  E <= 256, E N <= 2^30, K <= 2^20, n_rows <= 2^22 and n_rows N <= 2^39.
+ * Rows behind the last expert's stay as they were.  A negative count is taken as 0 and rows past
+ * n_rows are cut off; both are flagged (afd_ffn_rows_error).  The order of a row's sums depends on
+ * the sizes and on the counts, not on chance: equal calls give equal bits.  Everything belongs to
+ * the current device.  Asynchronous on `stream`; capturable after one call on the device. */
 int afd_ffn_w4_rows(const afd_ffn_w4 *w, int32_t E, const void *x, const int32_t *counts, int32_t n_rows,
                     void *y, int32_t y_dtype, void *stream);
 
@@ -377,9 +381,11 @@ int64_t afd_ffn_w4_scratch_bytes(int32_t n_rows, int32_t I);
  *         does (max |y| / 448, 1 for a zero row; nearest even, saturating), what
  *         afd_ffn_expert_rows_fp8 reads (both NULL: not written)
  * At least one of out and codes.  Strides are elements from row to row, at least H, 0 = H.  Any
- * alignment that the types allow is taken; where pointers and row strides are multiples of 16
- * bytes (codes: 8) and H of 8, rows move as 16-byte vectors.  Buffers must not overlap except
- * as said.  1 <= H <= 32768.  The sum of squares is in fp32: |s| up to 1e16 is in range.
+ * alignment that the types allow is taken.  Rows move as 16-byte pieces where pointers and row
+ * strides are multiples of 16 bytes (codes: 8) and H of 8; as shifted pieces where the outputs have
+ * no gaps between rows, start on such boundaries, and H >= 512; else element by element.  Buffers
+ * must not overlap except as said.  1 <= H <= 32768.  The sum of squares is in fp32: |s| up to 1e16
+ * is in range, and so are products s gamma in fp32's.
  * x, sum, out ... of token t are [t * stride, t * stride + H).  One launch; capturable. */
 typedef struct {
     int32_t T, H;
