@@ -46,7 +46,7 @@ struct W4Args {
   const __nv_bfloat16* x;   // [n_rows * planes][K]
   const int32_t* counts;    // [E], or nullptr: one expert, every row
   void* y;
-  int E, N, K, G, n_rows, scale_f32, y_f32;
+  int E, N, K, G, KG, n_rows, scale_f32, y_f32;  // KG = K / G
   unsigned group_inv;       // ceil(2^32 / (G / 32)), 0 for groups of 32
   int glog;                 // log2 G, where windows says so
   int windows;              // groups of 2^i, rows of scales (and zero points) that whole 16-byte pieces cover
@@ -119,42 +119,69 @@ struct UnitTables {
   int first[kW4MaxExperts], rows[kW4MaxExperts], unit_base[kW4MaxExperts + 1];
 };
 
-// Rows and unit bases of every expert from counts: negative counts are flagged and taken as 0,
-// rows past n_rows are flagged and cut off.  units_of(rows): an expert's units, asked of all threads after a
-// barrier.
-template <typename F>
-__device__ __forceinline__ void build_tables(const W4Args& a, F units_of, UnitTables& tb, int* wsum) {
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  int c = 0;
+// Rows of the lane's eight experts lane * 8 + i, by every warp for itself: with the experts spread over the
+// block the scans' barriers were a microsecond of a kernel's start.  Negative counts are flagged and
+// taken as 0, rows past n_rows are flagged and cut off.
+struct LaneRows {
+  int first[8], rows[8];
+};
+__device__ __forceinline__ LaneRows lane_rows(const W4Args& a, int lane) {
+  LaneRows r;
+  int c[8], sum = 0;
   bool bad = false;
-  if (tid < a.E) {
-    c = a.counts ? a.counts[tid] : a.n_rows;
-    bad = c < 0 || c > a.n_rows;
-    c = min(max(c, 0), a.n_rows);
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const int e = lane * 8 + i;
+    c[i] = e < a.E ? (a.counts ? a.counts[e] : a.n_rows) : 0;
   }
-  int incl = warp_incl_scan(c, lane);
-  if (lane == 31) wsum[warp] = incl;
-  __syncthreads();
-  int before = 0;
-  for (int w = 0; w < warp; ++w) before += wsum[w];
-  incl += before;
-  bad |= incl > a.n_rows;
-  const int first = min(incl - c, a.n_rows);
-  const int rows = min(c, a.n_rows - first);
-  if (bad && blockIdx.x == 0) atomicOr(a.err, kErrBadOffsets);
-  const int units = units_of(rows);  // by all threads; 0 rows past the last expert
-  int uincl = warp_incl_scan(units, lane);
-  __syncthreads();
-  if (lane == 31) wsum[warp] = uincl;
-  __syncthreads();
-  for (int w = 0; w < warp; ++w) uincl += wsum[w];
-  if (tid < kW4MaxExperts) {
-    tb.first[tid] = first;
-    tb.rows[tid] = rows;
-    tb.unit_base[tid + 1] = uincl;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    bad |= c[i] < 0 || c[i] > a.n_rows;
+    c[i] = min(max(c[i], 0), a.n_rows);
+    sum += c[i];
   }
-  if (tid == 0) tb.unit_base[0] = 0;
-  __syncthreads();
+  int at = warp_incl_scan(sum, lane) - sum;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    bad |= at + c[i] > a.n_rows;
+    r.first[i] = min(at, a.n_rows);
+    r.rows[i] = min(c[i], a.n_rows - r.first[i]);
+    at += c[i];
+  }
+  if (bad && blockIdx.x == 0 && threadIdx.x < 32) atomicOr(a.err, kErrBadOffsets);
+  return r;
+}
+
+// The tables of these experts with units[i] units each, written by the first warp; the total.
+__device__ __forceinline__ int store_tables(const LaneRows& r, const int (&units)[8], int lane, UnitTables& tb) {
+  int sum = 0;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) sum += units[i];
+  const int incl = warp_incl_scan(sum, lane);
+  if (threadIdx.x < 32) {
+    int at = incl - sum;
+    if (lane == 0) tb.unit_base[0] = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      at += units[i];
+      tb.first[lane * 8 + i] = r.first[i];
+      tb.rows[lane * 8 + i] = r.rows[i];
+      tb.unit_base[lane * 8 + i + 1] = at;
+    }
+  }
+  return __shfl_sync(0xffffffffu, incl, 31);
+}
+
+// Token tiles of all experts at 16, 32 and 64 columns (step 1), or at 16, 8 and 4 (step -1).
+template <int STEP>
+__device__ __forceinline__ void count_tiles(const int (&cols)[8], int (&tiles)[3]) {
+#pragma unroll
+  for (int j = 0; j < 3; ++j) {
+    int n = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) n += (cols[i] + (1 << (4 + j * STEP)) - 1) >> (4 + j * STEP);
+    tiles[j] = __reduce_add_sync(0xffffffffu, n);
+  }
 }
 
 // Group of the 32 inputs kq: kq / (G / 32).
@@ -269,7 +296,7 @@ int launch_w4(const afd_ffn_w4& w, int E, const void* x, const int32_t* counts, 
   a.x = static_cast<const __nv_bfloat16*>(x);
   a.counts = counts;
   a.y = y;
-  a.E = E; a.N = w.N; a.K = w.K; a.G = w.group; a.n_rows = n_rows;
+  a.E = E; a.N = w.N; a.K = w.K; a.G = w.group; a.KG = w.K / w.group; a.n_rows = n_rows;
   a.scale_f32 = w.scale_dtype == AFD_DT_F32;
   a.y_f32 = y_f32;
   const unsigned q = w.group / 32;

@@ -47,11 +47,11 @@ struct NarrowShape {
 // as equal, 18 experts of 3840 x 1024 took units of 64 rows and 59 us, where 128 rows take 50.  R rows leave R / 8 columns; tiles: token tiles of all experts at 16,
 // 8 and 4 columns.  A lane works out each candidate: one after another the divisions took 2 us of a kernel's
 // start.
-__device__ __forceinline__ NarrowShape choose_narrow(const int* tiles, int outs, int log_pair, int slices, int ctas, int wgs) {
+__device__ __forceinline__ NarrowShape choose_narrow(const int (&tiles)[3], int outs, int log_pair, int slices, int ctas, int wgs) {
   const int lane = threadIdx.x & 31, lr = 7 - (lane >> 1), split = lane & 1 ? wgs : 1;
   unsigned cost = 0xffffffffu;
   if (lane < 6) {
-    const unsigned units = tiles[lane >> 1] * (static_cast<unsigned>(outs + (1 << (lr - log_pair)) - 1) >> (lr - log_pair));
+    const unsigned units = (lane < 2 ? tiles[0] : lane < 4 ? tiles[1] : tiles[2]) * (static_cast<unsigned>(outs + (1 << (lr - log_pair)) - 1) >> (lr - log_pair));
     const unsigned steps = static_cast<unsigned>(slices + (128 >> lr) - 1) >> (7 - lr);
     const unsigned teams = ctas * (split == 1 ? wgs : 1);
     // up to 2^24 in floats, which is enough for a choice, with room for the candidate below it
@@ -105,8 +105,6 @@ w4_narrow_kernel(const __grid_constant__ NarrowMaps codes, const W4Args a) {
   extern __shared__ uint8_t smem_raw[];
   __shared__ UnitTables tb;                          // unit_base: token tiles of the experts before
   __shared__ uint16_t tile_of[4 * kW4MaxExperts];    // of a token tile: its expert, and its number there * 256
-  __shared__ int wsum[kThreads / 32];
-  __shared__ int tiles[3];
   __shared__ __align__(8) uint64_t bars[kWgs * (kStages + 1)];
   __shared__ uint32_t tmem_slot;
   __shared__ int abort_flag;
@@ -117,30 +115,34 @@ w4_narrow_kernel(const __grid_constant__ NarrowMaps codes, const W4Args a) {
   const int wg = warp >> 2, r = tid & 127;           // warpgroup; TMEM lane
   volatile int* abort = &abort_flag;
 
-  if (a.first) wait_dependency();
-  const int outs = MODE == kGateUp ? a.N / 2 : a.N;
-  if (tid < 3) tiles[tid] = 0;
-  const int slices = (a.K + S - 1) / S;
-  NarrowShape shape{};
-  build_tables(a, [&](int rows) {
-    if (rows * kPlanes > N) rows = 0;
-#pragma unroll
-    for (int i = 0; i < 3; ++i) {
-      const int n = __reduce_add_sync(0xffffffffu, (rows * kPlanes + (16 >> i) - 1) >> (4 - i));
-      if ((tid & 31) == 0 && n) atomicAdd(&tiles[i], n);
-    }
-    __syncthreads();
-    shape = choose_narrow(tiles, outs, kLogPair, slices, gridDim.x, kWgs);
-    return (rows * kPlanes + (1 << shape.log_rows) / 8 - 1) >> (shape.log_rows - 3);
-  }, tb, wsum);
-  const int n_tiles = tb.unit_base[a.E];
-  if (n_tiles == 0) {
-    wait_dependency();  // what follows may rely on the kernel before this one
-    return;
+  // what needs no input: barriers and TMEM
+  if (tid < kWgs * (kStages + 1)) {
+    mbar_init(smem_u32(&bars[tid]), 1);
+    fence_barrier_init();
   }
-  if (tid < a.E)
-    for (int i = tb.unit_base[tid]; i < tb.unit_base[tid + 1]; ++i)
-      tile_of[i] = static_cast<uint16_t>(tid | (i - tb.unit_base[tid]) << 8);
+  if (tid == 0) abort_flag = 0;
+  if (warp == 1) {
+    tmem_alloc(smem_u32(&tmem_slot), 512);
+    tmem_relinquish();
+  }
+  if (a.first) wait_dependency();
+  const int outs = MODE == kGateUp ? a.N / 2 : a.N, lane = tid & 31;
+  const int slices = (a.K + S - 1) / S;
+  const LaneRows mine = lane_rows(a, lane);
+  int cols8[8], tiles[3], units[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) cols8[i] = mine.rows[i] * kPlanes > N ? 0 : mine.rows[i] * kPlanes;
+  count_tiles<-1>(cols8, tiles);
+  const NarrowShape shape = choose_narrow(tiles, outs, kLogPair, slices, gridDim.x, kWgs);
+#pragma unroll
+  for (int i = 0; i < 8; ++i) units[i] = (cols8[i] + (1 << shape.log_rows) / 8 - 1) >> (shape.log_rows - 3);
+  const int n_tiles = store_tables(mine, units, lane, tb);
+  if (warp == 0) {
+    __syncwarp();
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      for (int t = 0; t < units[i]; ++t) tile_of[tb.unit_base[lane * 8 + i] + t] = static_cast<uint16_t>((lane * 8 + i) | t << 8);
+  }
   const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;
   uint8_t* const gbase = smem_raw + (base - smem_u32(smem_raw));
   constexpr int kRingOff = kWgs * L::kTokens, kWindowOff = kRingOff + kWgs * kStages * L::kStep;
@@ -148,26 +150,22 @@ w4_narrow_kernel(const __grid_constant__ NarrowMaps codes, const W4Args a) {
   uint8_t* const tokens_at = gbase + wg * L::kTokens;
   const int ring_off = kRingOff + wg * kStages * L::kStep;
   const uint32_t full = smem_u32(&bars[wg * (kStages + 1)]), mma_bar = full + 8 * kStages;
-  if (tid == 0) {
-    for (int i = 0; i < kWgs * (kStages + 1); ++i) mbar_init(smem_u32(&bars[i]), 1);
-    abort_flag = 0;
-    fence_barrier_init();
-  }
-  if (warp == 0) {
-    tmem_alloc(smem_u32(&tmem_slot), 512);
-    tmem_relinquish();
-  }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   launch_dependents();  // what follows allocates TMEM after this
   const uint32_t tmem = tmem_slot;
+  if (n_tiles == 0) {
+    wait_dependency();  // what follows may rely on the kernel before this one
+    if (warp == 1) tmem_dealloc(tmem, 512);
+    return;
+  }
   const uint32_t lanes = static_cast<uint32_t>(warp & 3) << 21;  // the warp's lane quarter
   const uint32_t tm_a = tmem + wg * L::kACols, tm_d = tmem + kWgs * L::kACols + wg * L::kAccs;
   const uint64_t desc0 = sw128_desc(tokens);
   constexpr uint32_t idesc = idesc_mn(128, N, false);
 
-  const int KG = a.K / a.G, cps = a.scale_f32 ? 4 : 2;
+  const int KG = a.KG, cps = a.scale_f32 ? 4 : 2;
   const int split = shape.split;
   int it = 0, issued = 0;                            // steps of this group: taken, and under way
 
@@ -181,11 +179,11 @@ w4_narrow_kernel(const __grid_constant__ NarrowMaps codes, const W4Args a) {
     constexpr int kOutRows = R >> kLogPair;            // outputs of a unit
     const int blocks = (outs + kOutRows - 1) / kOutRows;
     const int total = n_tiles * blocks;
-    const int ksteps = (slices + kStack - 1) / kStack, per = (ksteps + split - 1) / split;
+    const int ksteps = (slices + kStack - 1) / kStack, per = split == 1 ? ksteps : (ksteps + kWgs - 1) / kWgs;
     const int sub = split == 1 ? 0 : wg, team = split == 1 ? wg : 0;
     const int steps = max(0, min(per, ksteps - sub * per));
-    const int active = (ksteps + per - 1) / per;       // groups of a team with a step
-    const int teams = gridDim.x * (kWgs / split);
+    const int active = split == 1 ? 1 : (ksteps + per - 1) / per;  // groups of a team with a step
+    const int teams = gridDim.x * (split == 1 ? kWgs : 1);
     const int u0 = team * gridDim.x + blockIdx.x;
     const int row = r & (R - 1), q = ((warp & 3) * 32) >> LR;  // row of the unit, slice of the step
 
@@ -245,7 +243,6 @@ w4_narrow_kernel(const __grid_constant__ NarrowMaps codes, const W4Args a) {
       if (a.zero)
         for (int o = (sub * kStack + q) * 32; o < KG; o += split * kStack * 32) prefetch_l2(a.zero + at + o);
     };
-    prefetch_scales(u0);
     if (MODE == kDown) wait_dependency();
 
     // Tokens: a thread moves its piece of 8 inputs (kc) of rows n0 + kRows i of the tile, which are column
@@ -277,7 +274,6 @@ w4_narrow_kernel(const __grid_constant__ NarrowMaps codes, const W4Args a) {
       const At un = unit_of(u);
       const int cols = un.m * kPlanes;
       const size_t srow = scale_row(un);
-      prefetch_scales(u + teams);
       float acc[C];
 #pragma unroll
       for (int i = 0; i < C; ++i) acc[i] = 0.f;
@@ -372,6 +368,7 @@ w4_narrow_kernel(const __grid_constant__ NarrowMaps codes, const W4Args a) {
         load_window(sk + kStack * S);
         place_next = which;
       }
+      prefetch_scales(u + teams);
 #pragma unroll 1
       for (int s = 0; s < steps; ++s, ++it, sk += kStack * S) {
         // under way, the youngest last: (tokens of this step,) the next step's window
@@ -493,7 +490,7 @@ w4_narrow_kernel(const __grid_constant__ NarrowMaps codes, const W4Args a) {
   if (MODE != kDown) wait_dependency();  // what follows may rely on the kernel before this one
   tc_fence_before();
   __syncthreads();
-  if (warp == 0) {
+  if (warp == 1) {
     tc_fence_after();
     tmem_dealloc(tmem, 512);
   }

@@ -59,12 +59,12 @@ struct WideShape {
 // The shape of the least cost: a team takes ceil(units / teams) units of ceil(slices / split) steps and about
 // 1.5 more for the join; a step of 32 columns takes 1.2 and one of 64 twice the time of one of 16.
 // tiles: token tiles of all experts at 16, 32 and 64 columns.
-__device__ __forceinline__ WideShape choose_wide(const int* tiles, unsigned blocks, unsigned slices, unsigned ctas) {
+__device__ __forceinline__ WideShape choose_wide(const int (&tiles)[3], unsigned blocks, unsigned slices, unsigned ctas) {
   const int lane = threadIdx.x & 31, log = lane % 3, size = lane / 3;  // a lane for each candidate
   static_assert(kWgs == 4, "splits of 1, 2 and 4");
   unsigned cost = 0xffffffffu;
   if (lane < 9) {
-    const unsigned teams = ctas * (kWgs >> log), units = tiles[size] * blocks;
+    const unsigned teams = ctas * (kWgs >> log), units = (size == 0 ? tiles[0] : size == 1 ? tiles[1] : tiles[2]) * blocks;
     const float step = size == 0 ? 10.f : size == 1 ? 12.f : 20.f;
     const float c = static_cast<float>((units + teams - 1) / teams) *
                     (static_cast<float>((slices + (1u << log) - 1) >> log) * step + 15.f);
@@ -99,7 +99,6 @@ w4_wide_kernel(const __grid_constant__ CUtensorMap codes, const W4Args a) {
   constexpr int kOut = MODE == kGateUp ? kWideRows / 2 : kWideRows;
   extern __shared__ uint8_t smem_raw[];
   __shared__ UnitTables tb;
-  __shared__ int wsum[kWideThreads / 32];
   __shared__ __align__(8) uint64_t bars[kWgs * (kWideStages + 1)];
   __shared__ uint32_t tmem_slot;
   __shared__ int abort_flag;
@@ -110,31 +109,30 @@ w4_wide_kernel(const __grid_constant__ CUtensorMap codes, const W4Args a) {
   const int wg = warp >> 2, r = tid & 127;  // warpgroup; row of the unit, which is the TMEM lane
   volatile int* abort = &abort_flag;
 
-  if (a.first) wait_dependency();
-  const int outs = MODE == kGateUp ? a.N / 2 : a.N;
-  const int blocks = (outs + kOut - 1) / kOut;
-  __shared__ int tiles[3];
-  if (tid < 3) tiles[tid] = 0;
-  const int slices = (a.K + kSliceK - 1) / kSliceK;
-  WideShape shape{};
-  build_tables(a, [&](int rows) {
-    if (rows * kPlanes <= a.above) rows = 0;
-#pragma unroll
-    for (int i = 0; i < 3; ++i) {
-      const int n = __reduce_add_sync(0xffffffffu, (rows * kPlanes + (16 << i) - 1) >> (4 + i));
-      if ((tid & 31) == 0 && n) atomicAdd(&tiles[i], n);
-    }
-    __syncthreads();
-    shape = choose_wide(tiles, blocks, slices, gridDim.x);
-    const int tokens = shape.cols / kPlanes;
-    return (rows + tokens - 1) / tokens * blocks;
-  }, tb, wsum);
-  const int tile = shape.cols / kPlanes;
-  const int total = tb.unit_base[a.E];
-  if (total == 0) {
-    wait_dependency();  // what follows may rely on the kernel before this one
-    return;
+  // what needs no input: barriers and TMEM
+  if (tid < kWgs * (kWideStages + 1)) {
+    mbar_init(smem_u32(&bars[tid]), 1);
+    fence_barrier_init();
   }
+  if (tid == 0) abort_flag = 0;
+  if (warp == 1) {
+    tmem_alloc(smem_u32(&tmem_slot), 512);
+    tmem_relinquish();
+  }
+  if (a.first) wait_dependency();
+  const int outs = MODE == kGateUp ? a.N / 2 : a.N, lane = tid & 31;
+  const int blocks = (outs + kOut - 1) / kOut;
+  const int slices = (a.K + kSliceK - 1) / kSliceK;
+  const LaneRows mine = lane_rows(a, lane);
+  int cols8[8], tiles[3], units[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) cols8[i] = mine.rows[i] * kPlanes > a.above ? mine.rows[i] * kPlanes : 0;
+  count_tiles<1>(cols8, tiles);
+  const WideShape shape = choose_wide(tiles, blocks, slices, gridDim.x);
+  const int tile = shape.cols / kPlanes;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) units[i] = ((cols8[i] + shape.cols - 1) >> (shape.cols == 16 ? 4 : shape.cols == 32 ? 5 : 6)) * blocks;
+  const int total = store_tables(mine, units, lane, tb);
   const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;
   uint8_t* const gbase = smem_raw + (base - smem_u32(smem_raw));
   const uint32_t tokens = base + wg * kTokenBytes;                                             // this group's tokens
@@ -142,26 +140,21 @@ w4_wide_kernel(const __grid_constant__ CUtensorMap codes, const W4Args a) {
   const int ring_off = kWgs * kTokenBytes + wg * kWideStages * kCodeBytes;                     // and ring
   constexpr int kWindowOff = kWgs * (kTokenBytes + kWideStages * kCodeBytes);
   const uint32_t full = smem_u32(&bars[wg * (kWideStages + 1)]), mma_bar = full + 8 * kWideStages;
-  if (tid == 0) {
-    for (int i = 0; i < kWgs * (kWideStages + 1); ++i) mbar_init(smem_u32(&bars[i]), 1);
-    abort_flag = 0;
-    fence_barrier_init();
-    tma_prefetch_desc(&codes);
-  }
-  if (warp == 0) {
-    tmem_alloc(smem_u32(&tmem_slot), 512);
-    tmem_relinquish();
-  }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   launch_dependents();  // what follows allocates TMEM after this
   const uint32_t tmem = tmem_slot;
+  if (total == 0) {
+    wait_dependency();  // what follows may rely on the kernel before this one
+    if (warp == 1) tmem_dealloc(tmem, 512);
+    return;
+  }
   const uint32_t lanes = static_cast<uint32_t>(warp & 3) << 21;  // the warp's lane quarter
   const uint64_t desc0 = sw128_desc(tokens);
   const uint32_t tm_a = tmem + wg * 64, tm_d = tmem + 256 + wg * 64;
 
-  const int KG = a.K / a.G, cps = a.scale_f32 ? 4 : 2;
+  const int KG = a.KG, cps = a.scale_f32 ? 4 : 2;
   const int split = shape.split;
   const int sub = wg & (split - 1), team = wg / split;
   const int per = (slices + split - 1) / split;  // a group's consecutive slices
@@ -219,7 +212,6 @@ w4_wide_kernel(const __grid_constant__ CUtensorMap codes, const W4Args a) {
     if (a.zero)
       for (int o = sub * 32; o < KG; o += split * 32) prefetch_l2(a.zero + at + o);
   };
-  prefetch_scales(u0);
   if (MODE == kDown) wait_dependency();
 
   int it = 0, ce = 0;
@@ -443,7 +435,7 @@ w4_wide_kernel(const __grid_constant__ CUtensorMap codes, const W4Args a) {
   if (MODE != kDown) wait_dependency();  // what follows may rely on the kernel before this one
   tc_fence_before();
   __syncthreads();
-  if (warp == 0) {
+  if (warp == 1) {
     tc_fence_after();
     tmem_dealloc(tmem, 512);
   }
