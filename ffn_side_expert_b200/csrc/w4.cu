@@ -119,68 +119,50 @@ struct UnitTables {
   int first[kW4MaxExperts], rows[kW4MaxExperts], unit_base[kW4MaxExperts + 1];
 };
 
-// Rows of the lane's eight experts lane * 8 + i, by every warp for itself: with the experts spread over the
-// block the scans' barriers were a microsecond of a kernel's start.  Negative counts are flagged and
-// taken as 0, rows past n_rows are flagged and cut off.
-struct LaneRows {
-  int first[8], rows[8];
-};
-__device__ __forceinline__ LaneRows lane_rows(const W4Args& a, int lane) {
-  LaneRows r;
-  int c[8], sum = 0;
-  bool bad = false;
+// Rows of every expert from counts, by every warp for itself, a lane for an expert; the first warp writes them down.
+// Negative counts are flagged and taken as 0, rows past n_rows are flagged and cut off.  tiles: the token
+// tiles of all experts with cols_of(rows) columns, at 16, 32 and 64 columns (STEP 1) or at 16, 8 and 4 (STEP -1).
+// (Experts spread over the block, with its barriers, took a microsecond more of a kernel's start.  The code runs
+// once, so its length counts too.)
+template <int STEP, typename F>
+__device__ __forceinline__ void count_rows(const W4Args& a, F cols_of, UnitTables& tb, int (&tiles)[3]) {
+  const int lane = threadIdx.x & 31;
+  int before = 0, n[3] = {0, 0, 0};
+#pragma unroll 1
+  for (int e0 = 0; e0 < a.E; e0 += 32) {
+    const int e = e0 + lane;
+    int c = e < a.E ? (a.counts ? a.counts[e] : a.n_rows) : 0;
+    bool bad = c < 0 || c > a.n_rows;
+    c = min(max(c, 0), a.n_rows);
+    const int end = before + warp_incl_scan(c, lane);  // at most 256 * 2^22
+    bad |= end > a.n_rows;
+    const int first = min(end - c, a.n_rows), rows = min(c, a.n_rows - first);
+    before = __shfl_sync(0xffffffffu, end, 31);
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const int e = lane * 8 + i;
-    c[i] = e < a.E ? (a.counts ? a.counts[e] : a.n_rows) : 0;
-  }
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    bad |= c[i] < 0 || c[i] > a.n_rows;
-    c[i] = min(max(c[i], 0), a.n_rows);
-    sum += c[i];
-  }
-  int at = warp_incl_scan(sum, lane) - sum;
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    bad |= at + c[i] > a.n_rows;
-    r.first[i] = min(at, a.n_rows);
-    r.rows[i] = min(c[i], a.n_rows - r.first[i]);
-    at += c[i];
-  }
-  if (bad && blockIdx.x == 0 && threadIdx.x < 32) atomicOr(a.err, kErrBadOffsets);
-  return r;
-}
-
-// The tables of these experts with units[i] units each, written by the first warp; the total.
-__device__ __forceinline__ int store_tables(const LaneRows& r, const int (&units)[8], int lane, UnitTables& tb) {
-  int sum = 0;
-#pragma unroll
-  for (int i = 0; i < 8; ++i) sum += units[i];
-  const int incl = warp_incl_scan(sum, lane);
-  if (threadIdx.x < 32) {
-    int at = incl - sum;
-    if (lane == 0) tb.unit_base[0] = 0;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      at += units[i];
-      tb.first[lane * 8 + i] = r.first[i];
-      tb.rows[lane * 8 + i] = r.rows[i];
-      tb.unit_base[lane * 8 + i + 1] = at;
+    for (int j = 0; j < 3; ++j) n[j] += (cols_of(rows) + (1 << (4 + j * STEP)) - 1) >> (4 + j * STEP);
+    if (threadIdx.x < 32) {
+      tb.first[e] = first;
+      tb.rows[e] = rows;
+      if (bad && blockIdx.x == 0) atomicOr(a.err, kErrBadOffsets);
     }
   }
-  return __shfl_sync(0xffffffffu, incl, 31);
+#pragma unroll
+  for (int j = 0; j < 3; ++j) tiles[j] = __reduce_add_sync(0xffffffffu, n[j]);
 }
 
-// Token tiles of all experts at 16, 32 and 64 columns (step 1), or at 16, 8 and 4 (step -1).
-template <int STEP>
-__device__ __forceinline__ void count_tiles(const int (&cols)[8], int (&tiles)[3]) {
-#pragma unroll
-  for (int j = 0; j < 3; ++j) {
-    int n = 0;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) n += (cols[i] + (1 << (4 + j * STEP)) - 1) >> (4 + j * STEP);
-    tiles[j] = __reduce_add_sync(0xffffffffu, n);
+// Unit bases of every expert, by the first warp: units_of(rows) of an expert.
+template <typename F>
+__device__ __forceinline__ void base_units(const W4Args& a, F units_of, UnitTables& tb) {
+  const int lane = threadIdx.x;
+  __syncwarp();
+  int before = 0;
+  if (lane == 0) tb.unit_base[0] = 0;
+#pragma unroll 1
+  for (int e0 = 0; e0 < a.E; e0 += 32) {
+    const int e = e0 + lane, units = units_of(tb.rows[e]);
+    const int end = before + warp_incl_scan(units, lane);
+    tb.unit_base[e + 1] = end;
+    before = __shfl_sync(0xffffffffu, end, 31);
   }
 }
 

@@ -128,20 +128,17 @@ w4_narrow_kernel(const __grid_constant__ NarrowMaps codes, const W4Args a) {
   if (a.first) wait_dependency();
   const int outs = MODE == kGateUp ? a.N / 2 : a.N, lane = tid & 31;
   const int slices = (a.K + S - 1) / S;
-  const LaneRows mine = lane_rows(a, lane);
-  int cols8[8], tiles[3], units[8];
-#pragma unroll
-  for (int i = 0; i < 8; ++i) cols8[i] = mine.rows[i] * kPlanes > N ? 0 : mine.rows[i] * kPlanes;
-  count_tiles<-1>(cols8, tiles);
+  int tiles[3];
+  auto cols_of = [&](int rows) { return rows * kPlanes > N ? 0 : rows * kPlanes; };
+  count_rows<-1>(a, cols_of, tb, tiles);
   const NarrowShape shape = choose_narrow(tiles, outs, kLogPair, slices, gridDim.x, kWgs);
-#pragma unroll
-  for (int i = 0; i < 8; ++i) units[i] = (cols8[i] + (1 << shape.log_rows) / 8 - 1) >> (shape.log_rows - 3);
-  const int n_tiles = store_tables(mine, units, lane, tb);
+  const int n_tiles = shape.log_rows == 7 ? tiles[0] : shape.log_rows == 6 ? tiles[1] : tiles[2];
   if (warp == 0) {
+    auto tiles_of = [&](int rows) { return (cols_of(rows) + (1 << shape.log_rows) / 8 - 1) >> (shape.log_rows - 3); };
+    base_units(a, tiles_of, tb);
     __syncwarp();
-#pragma unroll
-    for (int i = 0; i < 8; ++i)
-      for (int t = 0; t < units[i]; ++t) tile_of[tb.unit_base[lane * 8 + i] + t] = static_cast<uint16_t>((lane * 8 + i) | t << 8);
+    for (int e = lane; e < a.E; e += 32)
+      for (int at = tb.unit_base[e], t = 0; at < tb.unit_base[e + 1]; ++at, ++t) tile_of[at] = static_cast<uint16_t>(e | t << 8);
   }
   const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;
   uint8_t* const gbase = smem_raw + (base - smem_u32(smem_raw));

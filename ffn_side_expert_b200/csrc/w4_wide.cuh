@@ -120,19 +120,17 @@ w4_wide_kernel(const __grid_constant__ CUtensorMap codes, const W4Args a) {
     tmem_relinquish();
   }
   if (a.first) wait_dependency();
-  const int outs = MODE == kGateUp ? a.N / 2 : a.N, lane = tid & 31;
+  const int outs = MODE == kGateUp ? a.N / 2 : a.N;
   const int blocks = (outs + kOut - 1) / kOut;
   const int slices = (a.K + kSliceK - 1) / kSliceK;
-  const LaneRows mine = lane_rows(a, lane);
-  int cols8[8], tiles[3], units[8];
-#pragma unroll
-  for (int i = 0; i < 8; ++i) cols8[i] = mine.rows[i] * kPlanes > a.above ? mine.rows[i] * kPlanes : 0;
-  count_tiles<1>(cols8, tiles);
+  int tiles[3];
+  auto cols_of = [&](int rows) { return rows * kPlanes > a.above ? rows * kPlanes : 0; };
+  count_rows<1>(a, cols_of, tb, tiles);
   const WideShape shape = choose_wide(tiles, blocks, slices, gridDim.x);
   const int tile = shape.cols / kPlanes;
-#pragma unroll
-  for (int i = 0; i < 8; ++i) units[i] = ((cols8[i] + shape.cols - 1) >> (shape.cols == 16 ? 4 : shape.cols == 32 ? 5 : 6)) * blocks;
-  const int total = store_tables(mine, units, lane, tb);
+  const int total = (shape.cols == 16 ? tiles[0] : shape.cols == 32 ? tiles[1] : tiles[2]) * blocks;
+  if (warp == 0)
+    base_units(a, [&](int rows) { return (cols_of(rows) + shape.cols - 1) / shape.cols * blocks; }, tb);
   const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;
   uint8_t* const gbase = smem_raw + (base - smem_u32(smem_raw));
   const uint32_t tokens = base + wg * kTokenBytes;                                             // this group's tokens
