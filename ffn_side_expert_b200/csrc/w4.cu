@@ -11,7 +11,7 @@
 // terms (hi + lo, 2^-17 relative), which are two columns of the down product.
 //
 // Both products run on the 5th-generation tensor cores with the unpacked weights as the A operand in TMEM:
-// experts with up to 16 columns (tokens, or planes of tokens) in w4_narrow.cuh, the others in
+// experts with few columns (tokens, or planes of tokens) in w4_narrow.cuh, the others in
 // w4_wide.cuh.  A warp's mma.sync on codes unpacked in registers, tried first, was bound by the same
 // unpacking with more instructions around it (one token's eight experts of H = 7168, I = 2048: 66 us
 // against 60; 128 rows on 64 experts of 4096 x 1024: 143 against 101).
@@ -51,7 +51,7 @@ struct W4Args {
   int glog;                 // log2 G, where windows says so
   int windows;              // groups of 2^i, rows of scales (and zero points) that whole 16-byte pieces cover
   int first;                // this kernel is the call's first: its inputs may come from the kernel before it
-  int above;                // w4_wide.cuh: the experts with more columns than this
+  int most, above;          // w4_narrow.cuh: the experts with at most so many columns; w4_wide.cuh: with more than
   int* err;
 };
 
@@ -290,13 +290,21 @@ int launch_w4(const afd_ffn_w4& w, int E, const void* x, const int32_t* counts, 
   while (a.glog < 31 && 1 << (a.glog + 1) <= w.group) ++a.glog;
   a.err = err;
   a.first = !after;
-  const bool more = static_cast<long long>(n_rows) * kPlanes > kNarrowN;
+  // One kernel or two.  Up to 16 columns are one tile of w4_narrow.cuh.  A second kernel takes 4 to 5 us to
+  // start, in which 32 MB of codes stream.  So a few more columns, spread over several experts, go there as
+  // further tiles (12 rows on 32 experts of 1664 x 512: 13.6 us, 15.5 us with a second kernel; 32 rows on 8
+  // experts of 2048 x 1024: 15.4 and 18.8 us evenly, 15.6 and 18.2 us all on one).  Small weights go to
+  // w4_wide.cuh alone (16 rows on 2 experts of 2048 x 1024, the product of K 1024 there: 13.6 us, 16.0 us as
+  // tiles), unless K is long, which units of few rows split better (16 rows on each of 8 experts of 256 x 512:
+  // 26 us with two a product, 17 us with one).
+  const long long columns = static_cast<long long>(n_rows) * kPlanes;
+  const bool light = static_cast<long long>(E) * w.N * (w.K / 2) <= 32 << 20 && w.K <= 1024;
+  const bool more = columns > (!counts || (light && E < 4) ? kNarrowN : E < 4 ? 2 * kNarrowN : kNarrowMost);
+  const bool small = more && light;
+  a.most = more ? kNarrowN : kNarrowMost;
+  a.above = small ? 0 : kNarrowN;
   const uint64_t row_bytes = w.K / 2, rows = static_cast<uint64_t>(E) * w.N;
   cudaError_t e = cudaSuccess;
-  // A second kernel takes about 5 us to start, in which 32 MB of codes stream: smaller weights go to one
-  // kernel, unless K is long, which units of few rows split better (16 rows on each of 8 experts of 256 x 512: 26 us with two a product, 17 us with one).
-  const bool small = static_cast<long long>(E) * w.N * (w.K / 2) <= 32 << 20 && w.K <= 1024;
-  a.above = small ? 0 : kNarrowN;
   if (!more || (counts && !small)) {
     const bool wide = w.group % 128 == 0;  // steps of 256 inputs
     NarrowMaps maps;

@@ -1,4 +1,4 @@
-// w4_narrow.cuh -- 4-bit products of the experts with at most 16 columns (tokens, or planes of tokens), on
+// w4_narrow.cuh -- 4-bit products of the experts with few columns (tokens, or planes of tokens), on
 // the 5th-generation tensor cores, as in w4_wide.cuh: codes unpacked into TMEM as the A operand.
 //
 // A step of a warpgroup is 128 TMEM lanes of S inputs each against a tile of 16 columns: S = 256, or 128
@@ -16,6 +16,7 @@
 namespace afd {
 
 constexpr int kNarrowN = 16;                                    // columns of an MMA
+constexpr int kNarrowMost = 64;                                 // columns of an expert, in tiles
 
 // S: inputs of a step.  Warpgroups, TMEM columns of a warpgroup's accumulators, ring stages, shared memory.
 template <int S>
@@ -104,7 +105,9 @@ w4_narrow_kernel(const __grid_constant__ NarrowMaps codes, const W4Args a) {
   static_assert(PARTS * N <= L::kAccs, "every part has an accumulator");
   extern __shared__ uint8_t smem_raw[];
   __shared__ UnitTables tb;                          // unit_base: token tiles of the experts before
-  __shared__ uint16_t tile_of[4 * kW4MaxExperts];    // of a token tile: its expert, and its number there * 256
+  // of a token tile: its expert, and its number there * 256.  At most four tiles an expert with 16 columns, or
+  // kNarrowMost columns in all, and one more an expert.
+  __shared__ uint16_t tile_of[4 * kW4MaxExperts];
   __shared__ __align__(8) uint64_t bars[kWgs * (kStages + 1)];
   __shared__ uint32_t tmem_slot;
   __shared__ int abort_flag;
@@ -129,7 +132,7 @@ w4_narrow_kernel(const __grid_constant__ NarrowMaps codes, const W4Args a) {
   const int outs = MODE == kGateUp ? a.N / 2 : a.N, lane = tid & 31;
   const int slices = (a.K + S - 1) / S;
   int tiles[3];
-  auto cols_of = [&](int rows) { return rows * kPlanes > N ? 0 : rows * kPlanes; };
+  auto cols_of = [&](int rows) { return rows > a.most / kPlanes ? 0 : rows * kPlanes; };
   count_rows<-1>(a, cols_of, tb, tiles);
   const NarrowShape shape = choose_narrow(tiles, outs, kLogPair, slices, gridDim.x, kWgs);
   const int n_tiles = shape.log_rows == 7 ? tiles[0] : shape.log_rows == 6 ? tiles[1] : tiles[2];
@@ -277,7 +280,7 @@ w4_narrow_kernel(const __grid_constant__ NarrowMaps codes, const W4Args a) {
 
       const __nv_bfloat16* src = a.x + static_cast<size_t>(un.first) * kPlanes * a.K + sub * per * kStack * S + kc * 8;
       int left = a.K - (sub * per * kStack * S + kc * 8);  // inputs from the piece of slice 0 to the end of its row
-      uint4 v[kAsync ? 1 : kMoves];
+      [[maybe_unused]] uint4 v[kAsync ? 1 : kMoves];
       auto load_tokens = [&](uint32_t to) {
 #pragma unroll
         for (int i = 0; i < kMoves; ++i) {

@@ -124,7 +124,7 @@ w4_wide_kernel(const __grid_constant__ CUtensorMap codes, const W4Args a) {
   const int blocks = (outs + kOut - 1) / kOut;
   const int slices = (a.K + kSliceK - 1) / kSliceK;
   int tiles[3];
-  auto cols_of = [&](int rows) { return rows * kPlanes > a.above ? rows * kPlanes : 0; };
+  auto cols_of = [&](int rows) { return rows > a.above / kPlanes ? rows * kPlanes : 0; };
   count_rows<1>(a, cols_of, tb, tiles);
   const WideShape shape = choose_wide(tiles, blocks, slices, gridDim.x);
   const int tile = shape.cols / kPlanes;

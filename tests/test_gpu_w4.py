@@ -406,3 +406,21 @@ def test_norm_selection_experts_and_combine_together(T):
     # the rows' own error, the weights' (64 u), the sum's (k + 1 steps), half a bf16 step
     tol = (rw[:, :, None] * (tr + (64 + k + 1) * U * np.abs(yr))).sum(1) * (1 + 2.0 ** -8) + 2.0 ** -8 * np.abs(ref)
     assert (np.abs(f64(out) - ref) <= tol).all()
+
+
+@pytest.mark.parametrize("group", [32, 64, 128, 256])
+@pytest.mark.parametrize("counts", [[0, 0, 64, 0, 0], [64, 0, 0, 0], [17, 1, 30, 16], [20, 0, 0, 0, 33, 0, 1, 9], [13, 19],
+                                    [0, 32, 0], [33, 0, 32], [0, 65, 0, 0], [32], [33]])
+@pytest.mark.parametrize("N,K", [(88, 512), (1208, 2048)])
+def test_few_columns_over_several_tiles(group, counts, N, K):
+    """Calls of at most 64 columns, and of one more, with experts of up to all of them."""
+    gen = torch.Generator().manual_seed(group + sum(counts))
+    E, n = len(counts), sum(counts)
+    w = W4(gen, E, N, K, group, group != 64)
+    x = rows_of(gen, n, K)
+    check_rows(w, E, x, counts, F32, N, K)
+    # counts that do not fit the rows are flagged; the rows stay in bounds
+    y = run_rows(w, E, x[:-1].cuda(), [c + 1 for c in counts], n - 1, F32, N)
+    assert afd.afd_ffn_rows_error() != afd.AFD_OK
+    assert (y[n - 1:] == 7.0).all()
+    assert afd.afd_ffn_rows_error() == afd.AFD_OK
