@@ -259,7 +259,8 @@ w4_narrow_kernel(const __grid_constant__ NarrowMaps codes, const W4Args a) {
     // Scales and zero points come in windows of 16 bytes of scales, by cp.async to a place of the
     // thread's own; a thread per row is 32 lines a load, so one load for eight groups matters.
     // Rows of an odd length or start are read group by group.
-    // Two windows of a thread: one in use, one on its way, asked for two steps ahead.
+    // Two windows of a thread: one in use, one on its way, asked for two steps ahead.  A commit group goes with
+    // each step all the same, so that the waits count groups alike; a unit's last steps have empty ones.
     constexpr int kWindows = kThreads * 16, kZeros = 2 * kWindows, kZeroWindows = kThreads * 8;
     const uint32_t wsc = base + kWindowOff + tid * 16, wz = base + kWindowOff + kZeros + tid * 8;
     const uint8_t* const wat = gbase + kWindowOff + tid * 16;
@@ -300,8 +301,10 @@ w4_narrow_kernel(const __grid_constant__ NarrowMaps codes, const W4Args a) {
       int window = -1, which = 0;               // the window asked for last, and its place
       int place = 0, place_next = 0;            // of this step's window and the next one's
       int sk = (sub * per * kStack + q) * S;  // first input of the lane's slice
-      auto load_window = [&](int k) {
-        if (a.windows) {
+      // mine: a step of this group's share.  A window of the step after it would be in flight, with nothing that
+      // waits for it, when the next unit's first one goes to the same place.
+      auto load_window = [&](int k, bool mine) {
+        if (mine && a.windows) {
           const int w = k >> (a.glog + wlog);
           if (w != window && k < a.K) {
             window = w;
@@ -361,11 +364,11 @@ w4_narrow_kernel(const __grid_constant__ NarrowMaps codes, const W4Args a) {
       };
 
       if (steps > 0) {
-        load_window(sk);
+        load_window(sk, true);
         place = which;
         load_tokens(buf * L::kTile);
         load_scales(sk);
-        load_window(sk + kStack * S);
+        load_window(sk + kStack * S, steps > 1);
         place_next = which;
       }
       prefetch_scales(u + teams);
@@ -430,7 +433,7 @@ w4_narrow_kernel(const __grid_constant__ NarrowMaps codes, const W4Args a) {
         if (s + 1 < steps) {
           load_scales(sk + kStack * S);
           load_tokens((buf ^ 1) * L::kTile);
-          load_window(sk + 2 * kStack * S);
+          load_window(sk + 2 * kStack * S, s + 2 < steps);
           place = place_next;
           place_next = which;
         }

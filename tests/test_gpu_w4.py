@@ -424,3 +424,70 @@ def test_few_columns_over_several_tiles(group, counts, N, K):
     assert afd.afd_ffn_rows_error() != afd.AFD_OK
     assert (y[n - 1:] == 7.0).all()
     assert afd.afd_ffn_rows_error() == afd.AFD_OK
+
+
+# ------------------------------------------------------------------ split units, one after another in a block
+def scattered(gen, shape, dtype, span=6):
+    """Scales that differ by up to 2^(2 span) from row to row and group to group."""
+    return (torch.exp2((2 * span) * torch.rand(shape, generator=gen) - span) / 64).to(dtype)
+
+
+def off_a_piece(t, n):
+    """The same values, contiguous, n elements behind a 16-byte boundary: scales like these are read one by one."""
+    to = torch.empty((t.numel() + n,), dtype=t.dtype, device="cuda")[n:].view(t.shape)
+    return to.copy_(t)
+
+
+@pytest.mark.parametrize("group,scales,zeros", [(32, F32, True), (32, BF16, False), (64, F32, False), (128, F32, True),
+                                                (128, BF16, True), (256, F32, False)])
+def test_split_units_one_after_another(group, scales, zeros):
+    """Three tokens, units of 128 weight rows, two a block, each split by K over the block's warpgroups: with
+    32 or 16 steps a unit, 2 rounds of a share (8 or 6 steps) cost less than whole units or ones of 64 or 32 rows.
+    A share that ends inside K must not ask for scales behind it: they would land, in no order, where the next
+    unit's first ones go.  The scales read in pieces give the bits of the scales read one by one, and the
+    definition's values (evaluated on the device in 64 bits)."""
+    gen = torch.Generator().manual_seed(group)
+    K = 4096
+    N = 2 * 128 * torch.cuda.get_device_properties(0).multi_processor_count - 40
+    codes = torch.randint(0, 256, (1, N, K // 2), dtype=torch.uint8, generator=gen).cuda()
+    scale = scattered(gen, (1, N, K // group), scales).cuda()
+    zero = torch.randint(0, 16, scale.shape, dtype=torch.uint8, generator=gen).cuda() if zeros else None
+    x = rows_of(gen, 3, K).cuda()
+    one_by_one = afd.w4_weights(codes, off_a_piece(scale, 4 // scale.element_size()),
+                                None if zero is None else off_a_piece(zero, 4), group)
+    pieces = afd.w4_weights(codes, scale, zero, group)
+
+    q = torch.stack((codes[0] & 15, codes[0] >> 4), 2).view(N, K // group, group).double()
+    z = 8.0 if zero is None else zero[0].double()[:, :, None]
+    w = ((q - z) * scale[0].double()[:, :, None]).view(N, K)
+    ref, a = f64(x.double() @ w.T), f64(x.double().abs() @ w.abs().T)
+    want = torch.empty((3, N), device="cuda")
+    assert afd.afd_ffn_w4_rows(one_by_one, 1, x, None, 3, want) == afd.AFD_OK
+    assert (np.abs(f64(want) - ref) <= rows_tol(a, ref, K, F32)).all()
+    ys = [torch.full((3, N), 7.0, device="cuda") for _ in range(10)]
+    for y in ys:
+        assert afd.afd_ffn_w4_rows(pieces, 1, x, None, 3, y) == afd.AFD_OK
+    assert all(torch.equal(y, want) for y in ys)
+    assert afd.afd_ffn_rows_error() == afd.AFD_OK
+
+
+@pytest.mark.parametrize("group", [32, 128])
+def test_split_units_of_a_whole_expert(group):
+    """The same in the down product (rows of two bf16 terms, moved by cp.async) of a dense expert."""
+    gen = torch.Generator().manual_seed(group + 1)
+    I = 4096
+    H = 2 * 128 * torch.cuda.get_device_properties(0).multi_processor_count - 128
+    made = []
+    for N, K in ((2 * I, H), (H, I)):
+        codes = torch.randint(0, 256, (1, N, K // 2), dtype=torch.uint8, generator=gen).cuda()
+        scale = (scattered(gen, (1, N, K // group), F32, 3) * K ** -0.5).cuda()
+        made.append((afd.w4_weights(codes, scale, None, group), afd.w4_weights(codes, off_a_piece(scale, 1), None, group)))
+    x = rows_of(gen, 3, H).cuda()
+    scratch = torch.empty((afd.afd_ffn_w4_scratch_bytes(3, I),), dtype=torch.uint8, device="cuda")
+    want = torch.empty((3, H), device="cuda")
+    assert afd.afd_ffn_w4_expert_rows(made[0][1], made[1][1], 1, x, None, 3, want, scratch) == afd.AFD_OK
+    ys = [torch.full((3, H), 7.0, device="cuda") for _ in range(10)]
+    for y in ys:
+        assert afd.afd_ffn_w4_expert_rows(made[0][0], made[1][0], 1, x, None, 3, y, scratch) == afd.AFD_OK
+    assert torch.isfinite(want).all() and all(torch.equal(y, want) for y in ys)
+    assert afd.afd_ffn_rows_error() == afd.AFD_OK
