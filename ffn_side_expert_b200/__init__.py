@@ -62,6 +62,7 @@ class afd_ffn_w4(ctypes.Structure):
     _fields_ = [("codes", ctypes.c_void_p), ("scale", ctypes.c_void_p), ("zero", ctypes.c_void_p),
                 ("N", ctypes.c_int32), ("K", ctypes.c_int32), ("group", ctypes.c_int32),
                 ("scale_dtype", ctypes.c_int32)]
+    experts = None  # matrices that the tensors hold, where w4_weights knows them
 
 
 class afd_ffn_norm_cfg(ctypes.Structure):
@@ -362,18 +363,29 @@ def w4_weights(codes, scale, zero=None, group=None) -> afd_ffn_w4:
         raise ValueError("zero is uint8")
     w = afd_ffn_w4(_ptr(codes), _ptr(scale), _ptr(zero), N, K, group, _dtype(scale))
     w._keep = (codes, scale, zero)
+    w.experts = codes.numel() // max(1, N * codes.shape[-1])
     return w
 
 
+def _holds(w, E):
+    """Whether the tensors of w have E matrices (nothing says so of a struct filled in by hand)."""
+    return w is None or w.experts is None or E <= w.experts
+
+
 def afd_ffn_w4_rows(w, E, x, counts, n_rows, y, y_dtype=None, stream=None) -> int:
-    """y_dtype defaults to the tensor's own."""
+    """y_dtype defaults to the tensor's own.  More experts than w4_weights was given are refused."""
+    if not _holds(w, E):
+        return AFD_ERR_INVALID_ARG
     if y_dtype is None:
         y_dtype = _dtype(y)
     return _lib.afd_ffn_w4_rows(_ref(w), E, _ptr(x), _ptr(counts), n_rows, _ptr(y), y_dtype, _stream(stream))
 
 
 def afd_ffn_w4_expert_rows(w13, w2, E, rows, counts, n_rows, Y, scratch, y_dtype=None, stream=None) -> int:
-    """y_dtype defaults to the tensor's own; scratch: afd_ffn_w4_scratch_bytes(n_rows, I) bytes."""
+    """y_dtype defaults to the tensor's own; scratch: afd_ffn_w4_scratch_bytes(n_rows, I) bytes.  More
+    experts than w4_weights was given are refused."""
+    if not (_holds(w13, E) and _holds(w2, E)):
+        return AFD_ERR_INVALID_ARG
     if y_dtype is None:
         y_dtype = _dtype(Y)
     return _lib.afd_ffn_w4_expert_rows(_ref(w13), _ref(w2), E, _ptr(rows), _ptr(counts), n_rows, _ptr(Y), y_dtype,

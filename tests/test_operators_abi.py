@@ -132,3 +132,19 @@ def test_struct_sizes_match_the_header():
     assert ctypes.sizeof(afd.afd_ffn_routing) == 24
     assert ctypes.sizeof(afd.afd_ffn_w4) == 40
     assert ctypes.sizeof(afd.afd_ffn_norm_cfg) == 56
+
+
+def test_w4_refuses_more_experts_than_its_tensors_hold():
+    """The library cannot see where the weights end; the binding knows the tensors it described."""
+    def plan(E, N, K):
+        shape = (E, N) if E else (N,)
+        return afd.w4_weights(torch.zeros(shape + (K // 2,), dtype=torch.uint8), torch.ones(shape + (K // 32,)))
+    for E, n in ((3, 3), (0, 1)):                        # a stack, one matrix
+        w13, w2 = plan(E, 256, 64), plan(E, 64, 128)
+        for e in (n, 1):                                 # the first ones of a stack are a stack
+            assert afd.afd_ffn_w4_rows(w2, e, A, A, 0, A, afd.AFD_DT_F32) == OK
+            assert afd.afd_ffn_w4_expert_rows(w13, w2, e, A, A, 0, A, A, afd.AFD_DT_F32) == OK
+        assert afd.afd_ffn_w4_rows(w2, n + 1, A, A, 0, A, afd.AFD_DT_F32) == BAD
+        assert afd.afd_ffn_w4_expert_rows(w13, w2, n + 1, A, A, 0, A, A, afd.AFD_DT_F32) == BAD
+        assert afd.afd_ffn_w4_expert_rows(plan(5, 256, 64), w2, n + 1, A, A, 0, A, A, afd.AFD_DT_F32) == BAD
+        assert afd.afd_ffn_w4_expert_rows(w13, plan(5, 64, 128), n + 1, A, A, 0, A, A, afd.AFD_DT_F32) == BAD
