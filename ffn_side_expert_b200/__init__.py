@@ -333,12 +333,15 @@ def _ref(struct):
 
 def afd_ffn_select_experts(logits, choice_bias, T, E, k, routing, topk_idx, topk_w, logits_dtype=None,
                            logits_stride=None, stream=None) -> int:
-    """logits_dtype and logits_stride default to the tensor's own."""
+    """logits_dtype and logits_stride default to the tensor's own: one whose experts do not lie side by side, or
+    whose tokens share a row, is refused."""
     if logits_dtype is None:
         logits_dtype = _dtype(logits)
-    if logits_stride is None:
+    if logits_stride is None and logits is not None:
         logits_stride = logits.stride(0) if T > 1 else 0
-    return _lib.afd_ffn_select_experts(_ptr(logits), logits_dtype, logits_stride, _ptr(choice_bias), T, E, k,
+        if (T > 1 and logits_stride == 0) or (T > 0 and E > 1 and logits.stride(-1) != 1):
+            return AFD_ERR_INVALID_ARG
+    return _lib.afd_ffn_select_experts(_ptr(logits), logits_dtype, logits_stride or 0, _ptr(choice_bias), T, E, k,
                                        _ref(routing), _ptr(topk_idx), _ptr(topk_w), _stream(stream))
 
 

@@ -148,3 +148,16 @@ def test_w4_refuses_more_experts_than_its_tensors_hold():
         assert afd.afd_ffn_w4_expert_rows(w13, w2, n + 1, A, A, 0, A, A, afd.AFD_DT_F32) == BAD
         assert afd.afd_ffn_w4_expert_rows(plan(5, 256, 64), w2, n + 1, A, A, 0, A, A, afd.AFD_DT_F32) == BAD
         assert afd.afd_ffn_w4_expert_rows(w13, plan(5, 64, 128), n + 1, A, A, 0, A, A, afd.AFD_DT_F32) == BAD
+
+
+@pytest.mark.parametrize("logits", [
+    torch.zeros((16, 4)).t(),                        # experts 4 elements apart
+    torch.zeros((4, 32))[:, ::2],
+    torch.zeros((1, 16)).expand(4, 16),              # one row for every token: its stride of 0 would mean E
+    torch.zeros((4, 1)).expand(4, 16),
+])
+def test_selection_refuses_logits_that_are_no_rows(logits):
+    """The stride is the tensor's own, so the binding can see that the rows are not there to be read."""
+    idx, w = torch.zeros((4, 2), dtype=torch.int32), torch.zeros((4, 2))
+    r = _routing(n_groups=1, topk_groups=1)
+    assert afd.afd_ffn_select_experts(logits, None, 4, 16, 2, r, idx, w) == BAD
