@@ -3,7 +3,7 @@
 //
 //   s = x + residual (fp32)      sum = s in the residual's type
 //   y = s * (mean(s^2) + eps)^(-1/2) * gamma (fp32, from s before its rounding)
-//   out = bf16(y)      row_scale = max |y| / 448 (1 for a zero row)      codes = e4m3(y / row_scale)
+//   out = bf16(y)      row_scale = max |y| / 448 (1 for a zero row, at least 2^-149)      codes = e4m3(y / row_scale)
 //
 // Bound by HBM: every byte is read and written once.  One CTA holds a row in registers between
 // the loads and the stores; its one reduction carries both sum(s^2) and max |s gamma|, since
@@ -89,6 +89,12 @@ __device__ __forceinline__ float divide(float a, float b, float r) {
   return fmaf(fmaf(-q, b, a), r, q);
 }
 
+// Scale of a row's codes.  A quotient that rounds to zero would make the codes those of y / 0, and NaN at the
+// row's zeros: the smallest fp32 number stands for it.
+__device__ __forceinline__ float row_scale_of(float amax) {
+  return amax > 0.f ? fmaxf(__fdiv_rn(amax, kE4m3Max), 0x1p-149f) : 1.0f;
+}
+
 // One CTA per row; thread i takes the pieces of V elements i, i + blockDim, ... (N at most) and keeps
 // s gamma in registers; sum is written on the way.  The sum of squares goes through shuffles, the
 // maximum through redux.sync on its bits; then every warp adds the warps' sums in the same order.
@@ -151,7 +157,7 @@ add_rmsnorm_kernel(const NormArgs a) {
   top = __uint_as_float(__reduce_max_sync(0xffffffffu, lane < warps ? red_top[lane] : 0u));
   const float factor = __frsqrt_rn(ss / static_cast<float>(a.H) + a.eps);
   const float amax = top * factor;
-  const float scale = amax > 0.f ? __fdiv_rn(amax, kE4m3Max) : 1.0f;
+  const float scale = row_scale_of(amax);
   const float inv = __frcp_rn(scale);
   const bool plain = scale > 1e-30f && scale < 1e30f;  // where divide() holds
 #pragma unroll
@@ -305,7 +311,7 @@ add_rmsnorm_shifted_kernel(const NormArgs a) {
   top = __uint_as_float(__reduce_max_sync(0xffffffffu, lane < warps ? red_top[lane] : 0u));
   const float factor = __frsqrt_rn(ss / static_cast<float>(a.H) + a.eps);
   const float amax = top * factor;
-  const float scale = amax > 0.f ? __fdiv_rn(amax, kE4m3Max) : 1.0f;
+  const float scale = row_scale_of(amax);
   const float inv = __frcp_rn(scale);
   const bool plain = scale > 1e-30f && scale < 1e30f;
 #pragma unroll

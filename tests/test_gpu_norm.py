@@ -248,3 +248,19 @@ def test_in_place_rows_of_any_start(H, rdt):
         x0, r0 = x.clone(), r.clone()
         call(x, r, g, r, x, None, None)
         check(x0, r0, g, r, x, None, None)
+
+
+@pytest.mark.parametrize("H", [256, 257, 513, 1024])
+def test_codes_of_rows_next_to_nothing(H):
+    """max |y| of 2^-149, whose 448th part is no fp32 number: the scale stays above zero, so the zeros of the
+    row have code 0 and not that of 0 / 0.  y: x gamma = 2^-133 1e-5 rounds to 2^-149, and the factor is 1."""
+    for T in (1, 300):
+        x = torch.zeros((T, H), dtype=BF16, device="cuda")
+        x[:, H // 2] = 2.0 ** -133
+        g = torch.full((H,), 1e-5, device="cuda")
+        codes = torch.zeros((T, H), dtype=torch.float8_e4m3fn, device="cuda")
+        scale = torch.zeros((T,), device="cuda")
+        call(x, None, g, None, None, codes, scale, eps=1.0)
+        got = f64(codes.float()) * f64(scale)[:, None]
+        assert (f64(scale) > 0).all() and np.isfinite(got).all()
+        assert (got[:, H // 2] == 2.0 ** -149).all() and np.count_nonzero(got) == T
