@@ -12,6 +12,8 @@
 #include <cuda_fp8.h>
 #include <cuda_runtime.h>
 
+#include <algorithm>
+
 #include "afd_ffn.h"
 #include "common.cuh"
 #include "internal.h"
@@ -383,7 +385,9 @@ constexpr int kShiftedMinH = 512;
 template <typename RT, typename GT>
 void launch_shifted(const NormArgs& a, int T, cudaStream_t s) {
   const int pieces = (a.H + 14) / 8;  // at most
-  const int per = pieces <= 256 ? 1 : pieces <= 1024 ? 2 : 5, threads = (pieces + per * 32 - 1) / (per * 32) * 32;
+  // At most 32 elements a thread, as in the other forms: a row of more than 4096 pieces is a thread's fifth one
+  // only where its first and last are parts.
+  const int per = pieces <= 256 ? 1 : pieces <= 1024 ? 2 : 4, threads = std::min(1024, (pieces + per * 32 - 1) / (per * 32) * 32);
   if (per == 1) launch_dependent(add_rmsnorm_shifted_kernel<1, 256, 4, RT, GT>, T, threads, 0, s, a);
   else if (per == 2) launch_dependent(add_rmsnorm_shifted_kernel<2, 512, 4, RT, GT>, T, threads, 0, s, a);
   else launch_dependent(add_rmsnorm_shifted_kernel<5, 1024, 1, RT, GT>, T, threads, 0, s, a);

@@ -264,3 +264,20 @@ def test_codes_of_rows_next_to_nothing(H):
         got = f64(codes.float()) * f64(scale)[:, None]
         assert (f64(scale) > 0).all() and np.isfinite(got).all()
         assert (got[:, H // 2] == 2.0 ** -149).all() and np.count_nonzero(got) == T
+
+
+@pytest.mark.parametrize("H", [8201, 9001, 16001, 24001, 32753, 32767])
+def test_scales_of_wide_rows_of_any_start(H):
+    """The derivation above counts at most 32 squares a thread: so too in the shifted form's longest rows.  The
+    row scale is the one fp32 result that shows the factor: within 34 u (32 u, the product and the quotient)."""
+    gen = torch.Generator().manual_seed(H)
+    for T in (3, 300):
+        _, x = strided(T, H, 1, BF16, gen)
+        _, r = strided(T, H, 3, F32, gen, 3.0)
+        g = torch.ones((H,), device="cuda")
+        codes = torch.zeros((T, H), dtype=torch.float8_e4m3fn, device="cuda")
+        scale = torch.zeros((T,), device="cuda")
+        call(x, r, g, None, None, codes, scale)
+        check(x, r, g, None, None, codes, scale)
+        want = op.add_rmsnorm(f64(x), f64(r), f64(g), 1e-6)[2]
+        assert (np.abs(f64(scale) - want) <= 34 * U * want).all()
