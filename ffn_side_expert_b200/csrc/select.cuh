@@ -217,6 +217,10 @@ __device__ __forceinline__ int order_candidates(const float* logits, int* order,
   return lane < min(a.k, n) ? order[lane] : -1;
 }
 
+// 1 / (1 + exp(-l)); from where exp(-l) nears the end of fp32 on as exp(l), which it is to far more than fp32.
+constexpr float kFarDown = -80.f;
+__device__ __forceinline__ float sigmoid_of(float l) { return l < kFarDown ? expf(l) : 1.f / (1.f + expf(-l)); }
+
 constexpr int kSelectWarps = 4;  // tokens per CTA
 
 template <typename LT>
@@ -414,11 +418,17 @@ select_experts_kernel(const SelectArgs a) {
     const float lmax = warp_max(lm);
     // far down a sigmoid is exp(l) to more than fp32, and its ratios are those of exp(l - lmax)
     const bool ratio = !a.sigmoid || lmax < -40.f;
-    if (mine >= 0) w = ratio ? expf(lm - lmax) : 1.f / (1.f + expf(-lm));
+    if (mine >= 0) w = ratio ? expf(lm - lmax) : sigmoid_of(lm);
     const float z = warp_sum(w);
-    if (mine >= 0) w = w / z * a.weight_scale;
+    // one far down beside a best that is not: its own score can be below fp32, its ratio to exp(lmax) is not
+    if (!ratio && lm < kFarDown) {
+      const float base = fminf(lmax, 0.f);
+      w = expf(lm - base) * (expf(base) / z) * a.weight_scale;
+    } else if (mine >= 0) {
+      w = w / z * a.weight_scale;
+    }
   } else if (mine >= 0) {
-    w = (a.sigmoid ? 1.f / (1.f + expf(-lm)) : expf(lm - top) / sum) * a.weight_scale;
+    w = (a.sigmoid ? sigmoid_of(lm) : expf(lm - top) / sum) * a.weight_scale;
   }
   if (lane < a.k) {
     a.idx[static_cast<size_t>(t) * a.k + lane] = mine;

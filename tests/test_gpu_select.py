@@ -250,3 +250,14 @@ def test_logits_that_differ_in_their_last_bits(groups, keep):
         base = np.float32(at).view(np.int32)
         l = (base + rng.integers(0, 24, size=(40, 64))).astype(np.int32).view(np.float32)
         check(torch.from_numpy(l.copy()).cuda(), None, 9, dict(PLAIN, n_groups=groups, topk_groups=keep))
+
+
+@pytest.mark.parametrize("top", [-39.5, -30.0, -5.0, 0.5, 20.0])
+def test_sigmoid_scores_far_below_the_best(top):
+    """Renormalised weights of scores whose 1 + exp(-l) overflows beside one that is less far down: they keep
+    their ratio.  Bound: exp(l - a) with |l - a| < 64 is within 32 u (half a step of l - a) and expf's 4 u, the
+    factor exp(a) / sum within 4 + 16 + 1 u, two products 2 u: 59 u, taken as 64 u, and 1e-37 as above."""
+    l = torch.tensor([[top, -79.0, -85.0, -88.5, -89.0, -91.0, -95.0, -100.0],
+                      [-100.0, -99.0, top, -90.0, top, -80.5, -81.0, -88.8]])
+    for scale in (1.0, 2.5):
+        check(l.cuda(), None, 8, dict(PLAIN, sigmoid=True, weight_scale=scale))
