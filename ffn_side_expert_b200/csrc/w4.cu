@@ -183,7 +183,8 @@ template <int MODE>
 __device__ __forceinline__ void store_out(const W4Args& a, int row, int out, int outs, float v, float up) {
   if (MODE == kGateUp) {
     const float act = v / (1.f + expf(-v)) * up;
-    const __nv_bfloat16 hi = __float2bfloat16_rn(act);
+    // a number that would round to an infinite high term is cut off to the last bf16: its low term has the rest
+    const __nv_bfloat16 hi = fabsf(act) < 0x1.FFp127f ? __float2bfloat16_rn(act) : __float2bfloat16_rz(act);
     // an infinite or NaN value is its own high term alone
     const __nv_bfloat16 lo = __float2bfloat16_rn(fabsf(act) < INFINITY ? act - __bfloat162float(hi) : 0.f);
     __nv_bfloat16* y = static_cast<__nv_bfloat16*>(a.y) + static_cast<size_t>(row) * 2 * outs + paired_place(out);

@@ -491,3 +491,26 @@ def test_split_units_of_a_whole_expert(group):
         assert afd.afd_ffn_w4_expert_rows(made[0][0], made[1][0], 1, x, None, 3, y, scratch) == afd.AFD_OK
     assert torch.isfinite(want).all() and all(torch.equal(y, want) for y in ys)
     assert afd.afd_ffn_rows_error() == afd.AFD_OK
+
+
+def test_swiglu_value_above_the_last_bf16():
+    """A SwiGLU value of 3.4e38 is an fp32 number but rounds to an infinite bf16: its two terms stay finite.
+    gate = 2^64, up = 3.4e38 / 2^64, a down weight of 2^-64 beside zeros."""
+    act = float(np.float32(3.4e38))
+    codes = lambda q: torch.from_numpy(op.w4_pack(q))[None].cuda()                     # noqa: E731
+    q13, q2 = np.full((64, 32), 8, np.uint8), np.full((32, 32), 8, np.uint8)
+    q13[0, 0] = q13[32, 0] = 9
+    q2[5, 0] = 9
+    s13 = torch.ones((1, 64, 1), device="cuda")
+    s13[0, 0], s13[0, 32] = 2.0 ** 64, act * 2.0 ** -64
+    w13 = afd.w4_weights(codes(q13), s13, None, 32)
+    w2 = afd.w4_weights(codes(q2), torch.full((1, 32, 1), 2.0 ** -64, device="cuda"), None, 32)
+    for n in (1, 40):                                    # few columns, and many
+        x = torch.zeros((n, 32), dtype=BF16, device="cuda")
+        x[:, 0] = 1
+        y = torch.full((n, 32), 7.0, device="cuda")
+        scratch = torch.empty((afd.afd_ffn_w4_scratch_bytes(n, 32),), dtype=torch.uint8, device="cuda")
+        assert afd.afd_ffn_w4_expert_rows(w13, w2, 1, x, None, n, y, scratch) == afd.AFD_OK
+        ref = np.zeros((n, 32))
+        ref[:, 5] = act * 2.0 ** -64
+        assert (np.abs(f64(y) - ref) <= 2.0 ** -16 * ref).all()
