@@ -346,7 +346,8 @@ def afd_ffn_select_experts(logits, choice_bias, T, E, k, routing, topk_idx, topk
 
 
 def afd_ffn_set_routing(h, routing, choice_bias=None) -> int:
-    """choice_bias is borrowed: keep it alive until the next afd_ffn_set_routing or destroy."""
+    """choice_bias is borrowed: keep it alive until the next afd_ffn_set_routing or destroy, and as long as a
+    graph that was captured while it was set is replayed."""
     return _lib.afd_ffn_set_routing(h, _ref(routing), _ptr(choice_bias))
 
 
@@ -511,6 +512,7 @@ class AfdFfn:
         if st != AFD_OK:
             raise AfdError(st, "afd_ffn_create_ex")
         self._events = None
+        self._choice_biases = []
 
     def close(self):
         if getattr(self, "h", None):
@@ -518,6 +520,7 @@ class AfdFfn:
                 raise RuntimeError("an FfnService is still running on this layer: stop it first")
             afd_ffn_destroy(self.h)
             self.h = None
+            self._choice_biases = []
 
     def __del__(self):
         try:
@@ -533,8 +536,11 @@ class AfdFfn:
         self._check(afd_ffn_route(self.h, hidden, T, topk_idx, topk_w, stream), "afd_ffn_route")
 
     def set_routing(self, routing, choice_bias=None):
+        """choice_bias is referenced until close(): a graph captured while it was set goes on reading it.  To
+        change a bias often, write the new values into one tensor."""
         self._check(afd_ffn_set_routing(self.h, routing, choice_bias), "afd_ffn_set_routing")
-        self._choice_bias = choice_bias
+        if choice_bias is not None and all(b is not choice_bias for b in self._choice_biases):
+            self._choice_biases.append(choice_bias)
 
     def permute(self, hidden, topk_idx, T, counts, offsets, pos, src, stream=None):
         self._check(afd_ffn_permute(self.h, hidden, topk_idx, T, counts, offsets, pos, src, stream),

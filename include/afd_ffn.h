@@ -150,9 +150,10 @@ int afd_ffn_select_experts(const void *logits, int32_t logits_dtype, int64_t log
 
 /* Make afd_ffn_route and every afd_ffn_forward* of the handle select and weigh experts this way
  * (the handle's router_bias, if any, is part of the logits).  choice_bias [E] fp32 (device) or
- * NULL: borrowed, read by each later call, must outlive them.  routing is copied; NULL (with
- * choice_bias NULL) restores the softmax top-k.  Host only; a graph captured before keeps the
- * routing it was captured with. */
+ * NULL: borrowed, read by each later call, must outlive them, and every graph that was captured
+ * while it was set.  routing is copied; NULL (with choice_bias NULL) restores the softmax top-k.
+ * Host only; a graph captured before keeps the routing it was captured with, the bias's address
+ * included. */
 int afd_ffn_set_routing(afd_ffn_handle *h, const afd_ffn_routing *routing, const float *choice_bias);
 
 /* Dispatch order and dispatched rows: each token's hidden state is sent to the experts it

@@ -261,3 +261,42 @@ def test_sigmoid_scores_far_below_the_best(top):
                       [-100.0, -99.0, top, -90.0, top, -80.5, -81.0, -88.8]])
     for scale in (1.0, 2.5):
         check(l.cuda(), None, 8, dict(PLAIN, sigmoid=True, weight_scale=scale))
+
+
+GROUPED = dict(sigmoid=True, n_groups=4, topk_groups=2, group_best=2, renormalise=True, weight_scale=2.5)
+
+
+def test_a_captured_forward_keeps_its_routing():
+    """A graph captured under one routing, replayed after another was set and the caller's bias is gone."""
+    cfg = synth.MoEConfig("routed", T=48, H=256, E=16, k=2, I=128, S=1, seed=44)
+    L = Layer(cfg, redraws={})
+    try:
+        def both(stream=None):
+            i = torch.zeros((48, 2), dtype=torch.int32, device="cuda")
+            w, out = torch.zeros((48, 2), device="cuda"), torch.zeros_like(L.h)
+            return (i, w, out), lambda: (L.mod.route(L.h, 48, i, w, stream), L.mod.forward(L.h, out, stream=stream))
+        plain, call = both()
+        call()
+        L.mod.set_routing(routing(GROUPED), torch.linspace(0.2, -0.2, 16, device="cuda"))
+        want, call = both()
+        call()
+        torch.cuda.synchronize()
+        assert not torch.equal(plain[0], want[0])
+        s = torch.cuda.Stream()
+        s.wait_stream(torch.cuda.current_stream())
+        graph = torch.cuda.CUDAGraph()
+        captured, call = both(s)
+        with torch.cuda.graph(graph, stream=s):
+            call()
+        L.mod.set_routing(None)
+        junk = [torch.full((16,), 9.0 * n, device="cuda") for n in range(64)]    # what a freed bias would become
+        again, call = both()
+        call()
+        for _ in range(3):
+            graph.replay()
+        torch.cuda.synchronize()
+        assert len(junk) == 64
+        assert all(torch.equal(a, b) for a, b in zip(captured, want))
+        assert all(torch.equal(a, b) for a, b in zip(again, plain))
+    finally:
+        L.close()

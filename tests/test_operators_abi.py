@@ -2,6 +2,7 @@
 reaches the device)."""
 import ctypes
 import math
+import weakref
 
 import pytest
 import torch
@@ -161,3 +162,24 @@ def test_selection_refuses_logits_that_are_no_rows(logits):
     idx, w = torch.zeros((4, 2), dtype=torch.int32), torch.zeros((4, 2))
     r = _routing(n_groups=1, topk_groups=1)
     assert afd.afd_ffn_select_experts(logits, None, 4, 16, 2, r, idx, w) == BAD
+
+
+def test_a_layer_keeps_the_biases_that_its_graphs_read(monkeypatch):
+    """A graph captured under an earlier routing reads that routing's bias: it lives as long as the layer."""
+    status = [OK]
+    monkeypatch.setattr(afd, "afd_ffn_set_routing", lambda h, routing, bias=None: status[0])
+    monkeypatch.setattr(afd, "afd_ffn_destroy", lambda h: None)
+    layer = object.__new__(afd.AfdFfn)
+    layer.h, layer._choice_biases = 1, []
+    first, second, refused = torch.zeros(4), torch.ones(4), torch.ones(4)
+    alive = [weakref.ref(t) for t in (first, second, refused)]
+    for bias in (first, second, first, None):
+        layer.set_routing(_routing(), bias)
+    assert len(layer._choice_biases) == 2                # a tensor set twice is held once
+    status[0] = BAD
+    with pytest.raises(afd.AfdError):
+        layer.set_routing(_routing(), refused)
+    del first, second, refused, bias
+    assert [r() is not None for r in alive] == [True, True, False]
+    layer.close()
+    assert [r() is not None for r in alive] == [False] * 3
