@@ -13,7 +13,8 @@ import torch
 
 import ffn_side_expert_b200 as afd
 import synth
-from layer_support import Layer
+from ffn_side_expert_b200.service import FfnService, Mailbox
+from layer_support import BF16_TOL, FP8_TOL, Layer, rel_max_err, to64
 from oracle import moe
 from oracle import operators as op
 
@@ -266,6 +267,46 @@ def test_sigmoid_scores_far_below_the_best(top):
 GROUPED = dict(sigmoid=True, n_groups=4, topk_groups=2, group_best=2, renormalise=True, weight_scale=2.5)
 
 
+def clear_tokens(logits, bias, k, r, margin=1e-4):
+    """Tokens whose groups and choices are decided by more than `margin` (4 groups, the best two of each)."""
+    got = []
+    for l in logits:
+        c = np.array(op.select_token(l.tolist(), bias, k, **r)[2]).reshape(4, -1)
+        worth = np.sort(c, 1)[:, -2:].sum(1)
+        kept = np.sort(c[worth >= np.sort(worth)[2]].reshape(-1))[::-1][: k + 1]
+        got.append(np.sort(worth)[2] - np.sort(worth)[1] > margin and (kept[:-1] - kept[1:]).min() > margin)
+    return np.array(got)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp8"])
+@pytest.mark.parametrize("T", [1, 64, 700])
+def test_forward_under_a_routing(dtype, T):
+    """Both kinds of weights, small and large micro-batches: the layer's output is that of the experts and
+    weights that afd_ffn_route reports, and those are the definition's where the logits' error (1e-5, as above)
+    cannot matter."""
+    cfg = synth.MoEConfig("routed", T=T, H=256, E=16, k=2, I=128, S=1, seed=43, dtype=dtype)
+    L = Layer(cfg, redraws={})
+    try:
+        bias = torch.linspace(-0.2, 0.2, 16)
+        L.mod.set_routing(routing(GROUPED), bias.cuda())
+        idx, w = L.route()
+        got = to64(L.forward())
+        assert L.mod.get_error() == afd.AFD_OK
+        b = bias.double().numpy()
+        logits = moe.router_logits(L.hidden, L.Wr, L.bias)
+        ri, rw = op.select_experts(logits, b, 2, **GROUPED)
+        clear = clear_tokens(logits, b, 2, GROUPED)
+        assert clear.sum() >= T // 2
+        assert np.array_equal(idx.cpu().numpy()[clear], ri[clear])
+        assert np.abs(w.double().cpu().numpy() - rw)[clear].max(initial=0) <= 2.5 * 2e-5
+        some = np.arange(T)[:: max(1, T // 64)]
+        ref = L.oracle(tokens=some, routing=(idx.cpu().numpy(), w.double().cpu().numpy()))["out"]
+        # the bars of the layer tests, times the weights' own scale
+        assert rel_max_err(got[some], ref) <= (FP8_TOL if dtype == "fp8" else BF16_TOL)
+    finally:
+        L.close()
+
+
 def test_a_captured_forward_keeps_its_routing():
     """A graph captured under one routing, replayed after another was set and the caller's bias is gone."""
     cfg = synth.MoEConfig("routed", T=48, H=256, E=16, k=2, I=128, S=1, seed=44)
@@ -298,5 +339,31 @@ def test_a_captured_forward_keeps_its_routing():
         assert len(junk) == 64
         assert all(torch.equal(a, b) for a, b in zip(captured, want))
         assert all(torch.equal(a, b) for a, b in zip(again, plain))
+    finally:
+        L.close()
+
+
+def test_a_service_serves_under_the_routing_that_was_set():
+    cfg = synth.MoEConfig("routed", T=32, H=256, E=16, k=2, I=128, S=1, seed=45)
+    L = Layer(cfg, redraws={})
+    try:
+        L.mod.set_routing(routing(GROUPED), torch.linspace(0.2, -0.2, 16, device="cuda"))
+        want = L.forward().cpu()
+        mb = Mailbox(2, 32, 256)
+        svc = FfnService(L.mod, mb)
+        try:
+            for slot, rows in ((0, 32), (1, 7)):
+                mb.write_input(slot, L.hidden[:rows])
+                mb.post(slot, rows)
+            got = []
+            for slot, rows in ((0, 32), (1, 7)):
+                mb.wait(slot, 60.0)
+                got.append(mb.output(slot)[:rows].clone())
+        finally:
+            stats = svc.stop()
+            mb.close()
+        assert stats.status == afd.AFD_OK and stats.device_status == afd.AFD_OK
+        assert torch.equal(got[0], want)
+        assert torch.equal(got[1], L.forward(T=7).cpu())
     finally:
         L.close()
