@@ -514,3 +514,139 @@ def test_swiglu_value_above_the_last_bf16():
         ref = np.zeros((n, 32))
         ref[:, 5] = act * 2.0 ** -64
         assert (np.abs(f64(y) - ref) <= 2.0 ** -16 * ref).all()
+
+
+# ------------------------------------------------------------------ calls that follow one another at once
+@pytest.mark.parametrize("captured", [False, True])
+def test_calls_that_nothing_waits_between(captured):
+    """Whole experts with few and with many rows, two kernels a product, on one scratch: the rows come from a
+    norm and the counts from a copy just before, other rows and counts of another call follow at once, and what
+    the call read and its scratch are overwritten behind it.  Each call's results are those of a call alone."""
+    gen = torch.Generator().manual_seed(14)
+    E, H, I, rounds = 6, 2048, 1536, 12
+    w13, w2 = W4(gen, E, 2 * I, H, 128, True), W4(gen, E, H, I, 64)
+    lots = [[70, 3, 0, 20, 1, 9], [1, 0, 40, 2, 60, 0], [0, 103, 0, 0, 0, 0]]
+    n = 103
+    counts = [torch.tensor(c, dtype=torch.int32, device="cuda") for c in lots]
+    xs = [rows_of(gen, n, H).cuda() for _ in lots]
+    gamma = (1 + 0.2 * torch.randn((H,), generator=gen)).cuda()
+    cfg = afd.afd_ffn_norm_cfg(T=n, H=H, residual_dtype=afd.AFD_DT_BF16, gamma_dtype=afd.AFD_DT_F32, eps=1e-6)
+    rows, now = torch.empty((n, H), dtype=BF16, device="cuda"), torch.empty((E,), dtype=torch.int32, device="cuda")
+    scratch = torch.empty((afd.afd_ffn_w4_scratch_bytes(n, I),), dtype=torch.uint8, device="cuda")
+
+    def one(i, y):
+        now.copy_(counts[i])
+        assert afd.afd_ffn_add_rmsnorm(cfg, xs[i], None, gamma, None, rows) == afd.AFD_OK
+        assert afd.afd_ffn_w4_expert_rows(w13.plan, w2.plan, E, rows, now, n, y, scratch) == afd.AFD_OK
+
+    want = []
+    for i in range(3):
+        y = torch.full((n, H), 7.0, device="cuda")
+        torch.cuda.synchronize()
+        one(i, y)
+        torch.cuda.synchronize()
+        want.append(y)
+        used = sum(lots[i])
+        ref = op.w4_expert_rows(f64(rows[:used]), w13, w2, lots[i])
+        tol = experts_tol(f64(rows[:used]), w13, w2, lots[i], ref, H, I, F32)
+        assert (np.abs(f64(y[:used]) - ref) <= tol).all() and (y[used:] == 7.0).all()
+    ys = [torch.full((n, H), 7.0, device="cuda") for _ in range(rounds)]
+
+    def chain():
+        for r, y in enumerate(ys):
+            one(r % 3, y)
+            if r % 2:                                    # else the next call's own kernels follow
+                scratch.fill_(255)
+                rows.fill_(float("nan"))
+                now.fill_(-1)
+
+    if captured:
+        s = torch.cuda.Stream()
+        s.wait_stream(torch.cuda.current_stream())
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=s):
+            chain()
+        for _ in range(3):
+            graph.replay()
+    else:
+        chain()
+    torch.cuda.synchronize()
+    assert all(torch.equal(y, want[r % 3]) for r, y in enumerate(ys))
+    assert afd.afd_ffn_rows_error() == afd.AFD_OK
+
+
+# ------------------------------------------------------------------ as many rows as a prompt has
+@pytest.mark.parametrize("group,zeros,scales", [(32, True, F32), (64, False, BF16), (128, True, BF16), (256, False, F32)])
+def test_thousands_of_rows(group, zeros, scales):
+    gen = torch.Generator().manual_seed(group + 7)
+    N, K = 328, 512
+    w = W4(gen, 1, N, K, group, zeros, scales)
+    check_rows(w, 1, rows_of(gen, 5001, K), None, F32, N, K)
+    E, counts = 7, [1500, 0, 17, 2049, 1, 64, 900]
+    w = W4(gen, E, N, K, group, zeros, scales)
+    check_rows(w, E, rows_of(gen, sum(counts), K), counts, BF16, N, K)
+
+
+@pytest.mark.parametrize("H,I,counts", [(256, 128, [4096] * 15 + [4095]), (1024, 384, [2900, 0, 1, 33, 5, 700, 0, 16]),
+                                        (512, 2048, [0, 0, 3000])])
+def test_experts_with_thousands_of_rows(H, I, counts):
+    gen = torch.Generator().manual_seed(H + len(counts))
+    E, n = len(counts), sum(counts)
+    w13, w2 = W4(gen, E, 2 * I, H, 128, True), W4(gen, E, H, I, 64, False, F32)
+    x = rows_of(gen, n, H)
+    c = torch.tensor(counts, dtype=torch.int32, device="cuda")
+    scratch = torch.empty((afd.afd_ffn_w4_scratch_bytes(n, I),), dtype=torch.uint8, device="cuda")
+    ref = op.w4_expert_rows(f64(x), w13, w2, counts)
+    y = torch.full((n, H), 7.0, device="cuda")
+    assert afd.afd_ffn_w4_expert_rows(w13.plan, w2.plan, E, x.cuda(), c, n, y, scratch) == afd.AFD_OK
+    torch.cuda.synchronize()
+    assert (np.abs(f64(y) - ref) <= experts_tol(f64(x), w13, w2, counts, ref, H, I, F32)).all()
+    assert afd.afd_ffn_rows_error() == afd.AFD_OK
+
+
+@pytest.mark.parametrize("T", [3, 70])
+def test_tokens_with_no_expert_left(T):
+    """Selection, dispatch, 4-bit experts and combine where masks leave a token fewer experts than k, or none: the
+    empty slots are skipped and flagged, the rows behind the last expert's are nobody's, and a token with no
+    expert gets zeros."""
+    gen = torch.Generator().manual_seed(30 + T)
+    H, I, E, k = 256, 128, 8, 4
+    hidden = torch.randn((T, H), generator=gen).to(BF16).cuda()
+    logits = torch.randn((T, E), generator=gen)
+    logits[0] = float("-inf")
+    logits[1, 2:] = torch.finfo(F32).min                  # the type's lowest value is a number: chosen last
+    logits[2, 1:] = float("nan")
+    w13, w2 = W4(gen, E, 2 * I, H, 64, True), W4(gen, E, H, I, 32)
+    r = dict(sigmoid=False, n_groups=1, topk_groups=1, group_best=1, renormalise=True, weight_scale=1.0)
+    route = afd.afd_ffn_routing(score=0, n_groups=1, topk_groups=1, group_best=1, renormalise=1, weight_scale=1.0)
+    i32 = lambda *s: torch.full(s, -9, dtype=torch.int32, device="cuda")               # noqa: E731
+    idx, w, counts, offsets, pos, src = i32(T, k), torch.empty((T, k), device="cuda"), i32(E), i32(E + 1), i32(T, k), i32(T * k)
+    rows = torch.full((T * k, H), float("nan"), dtype=BF16, device="cuda")
+    Y, out = torch.full((T * k, H), float("nan"), device="cuda"), torch.full((T, H), 7.0, dtype=BF16, device="cuda")
+    scratch_d = i32(2 * ((T + 127) // 128) * E)
+    scratch_w = torch.empty((afd.afd_ffn_w4_scratch_bytes(T * k, I),), dtype=torch.uint8, device="cuda")
+    ok = afd.AFD_OK
+    assert afd.afd_ffn_select_experts(logits.cuda(), None, T, E, k, route, idx, w) == ok
+    assert afd.afd_ffn_dispatch_rows(hidden, idx, T, k, E, H, counts, offsets, pos, src, rows, scratch_d) == ok
+    assert afd.afd_ffn_w4_expert_rows(w13.plan, w2.plan, E, rows, counts, T * k, Y, scratch_w) == ok
+    assert afd.afd_ffn_combine_rows(Y, None, w, pos, T, k, H, out) == ok
+    torch.cuda.synchronize()
+    assert afd.afd_ffn_rows_error() == afd.AFD_ERR_DEVICE_FLAG          # the slots without an expert
+    assert afd.afd_ffn_rows_error() == ok
+    ri, rw = op.select_experts(logits.double().numpy(), None, k, **r)
+    assert np.array_equal(idx.cpu().numpy(), ri)
+    assert (ri[0] == -1).all() and (ri[2] == [0, -1, -1, -1]).all() and (ri[1] >= 0).all()
+    used = int((ri >= 0).sum())
+    assert torch.isnan(Y[used:]).all() and torch.isfinite(Y[:used]).all()
+    flat = ri.reshape(-1)
+    order = np.argsort(np.where(flat < 0, E, flat), kind="stable")[:used]
+    cnt = np.bincount(flat[flat >= 0], minlength=E).tolist()
+    assert counts.tolist() == cnt
+    xr = f64(hidden)[order // k]
+    ref_rows = op.w4_expert_rows(xr, w13, w2, cnt)
+    yr, tr = np.zeros((T * k, H)), np.zeros((T * k, H))
+    yr[order], tr[order] = ref_rows, experts_tol(xr, w13, w2, cnt, ref_rows, H, I, F32)
+    yr, tr = yr.reshape(T, k, H), tr.reshape(T, k, H)
+    ref = (rw[:, :, None] * yr).sum(1)
+    tol = (rw[:, :, None] * (tr + (64 + k + 1) * U * np.abs(yr))).sum(1) * (1 + 2.0 ** -8) + 2.0 ** -8 * np.abs(ref)
+    assert (np.abs(f64(out) - ref) <= tol).all() and (out[0] == 0).all()
