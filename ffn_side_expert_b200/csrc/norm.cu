@@ -1,5 +1,5 @@
 // norm.cu -- residual addition and root-mean-square norm in front of the FFN, with bf16 rows
-// for the router and the bf16 experts and e4m3 rows with one scale each for the W8A8 ones.
+// for the router and the layer, and e4m3 rows with one scale each for a W8A8 expert that takes every row.
 //
 //   s = x + residual (fp32)      sum = s in the residual's type
 //   y = s * (mean(s^2) + eps)^(-1/2) * gamma (fp32, from s before its rounding)

@@ -379,14 +379,18 @@ int64_t afd_ffn_w4_scratch_bytes(int32_t n_rows, int32_t I);
  *   out   y as bf16, what afd_ffn_route / afd_ffn_forward read (NULL: not written); it may be x's
  *         own buffer, with the same stride
  *   codes [T][H] e4m3 and row_scale [T]: y quantised with one scale per row as the W8A8 path
- *         does (max |y| / 448, 1 for a zero row; nearest even, saturating), what
- *         afd_ffn_expert_rows_fp8 reads (both NULL: not written)
+ *         does (max |y| / 448, 1 for a zero row, never below 2^-149; nearest even, saturating;
+ *         both NULL: not written).  Rows are in token order: what afd_ffn_expert_rows_fp8 reads
+ *         for an expert that takes every row, such as a dense FFN or a replicated shared
+ *         expert.  Routed experts read rows grouped by expert, which afd_ffn_forward and
+ *         afd_ffn_dispatch_rows_fp8 quantise from the bf16 rows, `out`
  * At least one of out and codes.  Strides are elements from row to row, at least H, 0 = H.  Any
  * alignment that the types allow is taken.  Rows move as 16-byte pieces where pointers and row
  * strides are multiples of 16 bytes (codes: 8) and H of 8; as shifted pieces where the outputs have
  * no gaps between rows, start on such boundaries, and H >= 512; else element by element.  Buffers
  * must not overlap except as said.  1 <= H <= 32768.  The sum of squares is in fp32: |s| up to 1e16
- * is in range, and so are products s gamma in fp32's.
+ * is in range, and on the small side a root mean square of 1e-18, or any with eps >= 1e-36;
+ * products s gamma are to be in fp32's normal range.
  * x, sum, out ... of token t are [t * stride, t * stride + H).  One launch; capturable. */
 typedef struct {
     int32_t T, H;

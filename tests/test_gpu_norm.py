@@ -18,6 +18,9 @@ import pytest
 import torch
 
 import ffn_side_expert_b200 as afd
+import synth
+from layer_support import FP8_TOL, Layer, rel_max_err
+from oracle import moe
 from oracle import operators as op
 
 pytestmark = pytest.mark.gpu
@@ -281,3 +284,29 @@ def test_scales_of_wide_rows_of_any_start(H):
         check(x, r, g, None, None, codes, scale)
         want = op.add_rmsnorm(f64(x), f64(r), f64(g), 1e-6)[2]
         assert (np.abs(f64(scale) - want) <= 34 * U * want).all()
+
+
+def test_codes_feed_a_dense_w8a8_expert():
+    """Codes and scales as they come, in token order, into an expert that takes every row (a dense FFN or a
+    replicated shared expert): against the definition of the expert on the dequantised rows."""
+    T, H, I = 40, 512, 256
+    cfg = synth.MoEConfig("dense", T=T, H=H, E=1, k=1, I=I, S=0, seed=51, dtype="fp8")
+    L = Layer(cfg, redraws={})
+    try:
+        gen = torch.Generator().manual_seed(52)
+        _, x = strided(T, H, 0, BF16, gen)
+        _, r = strided(T, H, 0, BF16, gen)
+        g = (1 + 0.2 * torch.randn((H,), generator=gen)).cuda()
+        total, codes = torch.empty_like(r), torch.empty((T, H), dtype=torch.float8_e4m3fn, device="cuda")
+        scale, Y = torch.empty((T,), device="cuda"), torch.empty((T, H), dtype=BF16, device="cuda")
+        call(x, r, g, total, None, codes, scale)
+        counts = torch.tensor([T], dtype=torch.int32, device="cuda")
+        assert afd.afd_ffn_expert_rows_fp8(L.mod.h, codes, scale, counts, T, Y) == afd.AFD_OK
+        torch.cuda.synchronize()
+        assert L.mod.get_error() == afd.AFD_OK
+        check(x, r, g, total, None, codes, scale)
+        w13, w2 = moe.expert_weights_f64(L.expert_fn(0))
+        ref = moe.swiglu_ffn(f64(codes.float()) * f64(scale)[:, None], w13, w2, quant_act=True)[0]
+        assert rel_max_err(f64(Y), ref) <= FP8_TOL
+    finally:
+        L.close()
