@@ -33,7 +33,7 @@ int rows_cuda_fail(cudaError_t e);
 int rows_err_word(int** out);
 
 // Descriptor of a matrix of `rows` rows of row_bytes bytes (16-byte aligned), boxes of box_rows rows x
-// box_bytes (64) bytes with the 64-byte swizzle, zero fill outside.
+// box_bytes (64 or 128) bytes with the swizzle of that many bytes, zero fill outside.
 bool encode_byte_rows(CUtensorMap* m, const void* base, uint64_t row_bytes, uint64_t rows, uint32_t box_bytes,
                       uint32_t box_rows);
 

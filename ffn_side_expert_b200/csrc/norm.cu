@@ -357,7 +357,8 @@ void launch_norm_kernel(const NormArgs& a, int T, cudaStream_t s) {
 // fill the SMs many times: two, so that a row's reduction is paid by fewer warps, in few enough
 // registers that four rows are in flight on an SM.  8192 rows of 7168 (bf16 residual, both outputs):
 // 98 us so (82 % of the copy rate); 1 piece 118 to 122 us, 4 pieces 112 to 139 us, 2 pieces in more
-// registers 110 us.  515 rows of 4097 single elements: 6 a thread 9.1 us, 5 10.7, 8 10.1, 16 13.9 us.
+// registers 110 us.  Single elements, which rows of any start take where an output has gaps between its
+// rows: 515 rows of 4097 at 6 a thread 9.1 us, 5 10.7, 8 10.1, 16 13.9 us.
 constexpr int kManyRows = 256;
 
 template <int V, typename RT, typename GT>

@@ -18,8 +18,13 @@ __device__ __forceinline__ uint32_t smem_u32(const void* p) {
 
 // ------------------------------------------------------------------ programmatic launches
 // A kernel launched as its predecessor's dependent (internal.h: launch_dependent) starts when every CTA
-// of that one has called launch_dependents or ended, and reads or writes nothing that another
-// kernel touches before wait_dependency, which returns when the predecessor's writes are visible.
+// of that one has called launch_dependents or ended.  wait_dependency returns when that one kernel has
+// ended and its writes are visible.  Rules:
+// - Before it waits, a kernel reads or writes nothing that a kernel before it may still touch.  That is nothing but
+//   its own shared memory and TMEM, unless kernels that are launched together see to more: in w4.cu the first one
+//   of a call calls launch_dependents behind its own wait, so all that came before the call has ended by the time
+//   that any of the others starts.
+// - Every kernel waits before it ends, so that the end of one means the end of all before it.
 __device__ __forceinline__ void launch_dependents() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 __device__ __forceinline__ void wait_dependency() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 

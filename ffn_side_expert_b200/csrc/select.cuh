@@ -48,9 +48,10 @@ struct SelectArgs {
 
 // Bounds on the fp32 scores' error, in steps of 2^-24 and against the largest score of the row.
 // sigmoid 1 / (1 + z): expf's 2 ulp (4 steps) times z / (1 + z) <= 1, the addition 1, the division
-// 1: 6 steps = 3.6e-7, taken as 4e-7.  softmax: the subtraction |l - max| exp(l - max) <= 0.4, expf 4, the sum's own terms
-// 4 + 0.4, its 8 additions in a lane and 5 between lanes, the division 1: 23 steps = 1.4e-6, taken
-// as 2e-6.  The sum with the bias rounds by 1 step of |c|, taken as 2.
+// 1: 6 steps = 3.6e-7, taken as 4e-7.  softmax: the subtraction |l - max| exp(l - max) <= 0.4, expf 4, the
+// sum's own terms 4 and their subtractions' mean under the softmax (|l - max| on average: at most 3.4 for 256
+// experts, one at the maximum and the others 4.3 below), its 8 additions in a lane and 5 between
+// lanes, the division 1: 26 steps = 1.55e-6, taken as 2e-6.  The sum with the bias rounds by 1 step of |c|, taken as 2.
 constexpr float kSigmoidErr = 4e-7f, kSoftmaxErr = 2e-6f;
 constexpr float kSumErr = 1.2e-7f;
 

@@ -40,7 +40,6 @@ constexpr int kW4MaxRows = 1 << 22;
 constexpr int kSliceK = 128;       // inputs of a slice of K
 
 struct W4Args {
-  const uint8_t* codes;
   const void* scale;
   const uint8_t* zero;
   const __nv_bfloat16* x;   // [n_rows * planes][K]
@@ -50,7 +49,10 @@ struct W4Args {
   unsigned group_inv;       // ceil(2^32 / (G / 32)), 0 for groups of 32
   int glog;                 // log2 G, where windows says so
   int windows;              // groups of 2^i, rows of scales (and zero points) that whole 16-byte pieces cover
-  int first;                // this kernel is the call's first: its inputs may come from the kernel before it
+  // The call's first kernel waits for the stream's kernel before it and only then lets the next one start.  So a
+  // later kernel of the call may read counts, and all but the down products the rows, and write results and
+  // scratch, before its own wait; that one (at the start of kDown, else at the end) is for the kernel just before.
+  int first;
   int most, above;          // w4_narrow.cuh: the experts with at most so many columns; w4_wide.cuh: with more than
   int* err;
 };
@@ -219,10 +221,11 @@ int check_w4(const afd_ffn_w4* w, int32_t E) {
   return AFD_OK;
 }
 
-// Units are counted in 32 bits: blocks of at least 16 outputs for up to four token tiles of every expert, and
-// tiles of at least 8 tokens by 64 outputs.
+// Units are counted in 32 bits.  w4_narrow.cuh: blocks of at least 16 outputs, for token tiles of at least 4
+// columns: four of each expert with up to 16 columns, or of a call with up to 64 columns a full tile for each 4
+// and one more an expert.  w4_wide.cuh: tiles of at least 8 tokens by 64 outputs.
 bool units_fit(int n_rows, int E, int outs) {
-  const long long narrow = 4LL * E * (outs / 16 + 1);
+  const long long narrow = std::max(4LL * E, 16LL + E) * (outs / 16 + 1);
   const long long wide = (static_cast<long long>(n_rows) / 8 + E) * (outs / 64 + 1);
   return narrow < (1LL << 31) - 65536 && wide < (1LL << 31) - 65536;
 }
@@ -273,7 +276,6 @@ int launch_w4(const afd_ffn_w4& w, int E, const void* x, const int32_t* counts, 
               bool after, cudaStream_t s) {
   constexpr int kPlanes = MODE == kDown ? 2 : 1;
   W4Args a{};
-  a.codes = static_cast<const uint8_t*>(w.codes);
   a.scale = w.scale;
   a.zero = w.zero;
   a.x = static_cast<const __nv_bfloat16*>(x);

@@ -128,7 +128,7 @@ w4_narrow_kernel(const __grid_constant__ NarrowMaps codes, const W4Args a) {
     tmem_alloc(smem_u32(&tmem_slot), 512);
     tmem_relinquish();
   }
-  if (a.first) wait_dependency();
+  if (a.first) wait_dependency();  // else the call's first kernel has, before this one could start (W4Args::first)
   const int outs = MODE == kGateUp ? a.N / 2 : a.N, lane = tid & 31;
   const int slices = (a.K + S - 1) / S;
   int tiles[3];
@@ -153,7 +153,9 @@ w4_narrow_kernel(const __grid_constant__ NarrowMaps codes, const W4Args a) {
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  launch_dependents();  // what follows allocates TMEM after this
+  // What follows allocates TMEM after this.  It must stay behind the wait above: a call's next kernel reads counts,
+  // and rows, as soon as it starts, on the strength of that wait.
+  launch_dependents();
   const uint32_t tmem = tmem_slot;
   if (n_tiles == 0) {
     wait_dependency();  // what follows may rely on the kernel before this one

@@ -1,5 +1,5 @@
-// w4_wide.cuh -- 4-bit products of the experts with more rows than a unit of w4.cu's kernel takes, on
-// the 5th-generation tensor cores.
+// w4_wide.cuh -- 4-bit products of the experts with more columns (tokens, or planes of tokens) than
+// w4_narrow.cuh takes, on the 5th-generation tensor cores.
 //
 // A unit is 128 weight rows (SwiGLU: 64 gate rows and their 64 up rows) and up to 64 columns (tokens,
 // or planes of tokens).  A warpgroup's thread owns a weight row, that is a TMEM lane: it unpacks the
@@ -9,7 +9,7 @@
 // One accumulator per group of inputs; the thread adds it, times the group's scale, to its row's
 // sums in registers: fp32 throughout, and (q - z) / 4 is exact.
 //
-// What bounds it: unpacking, as in w4.cu, but once per 64 columns.  Four warpgroups work on their
+// What bounds it: unpacking (w4.cu), once per 64 columns.  Four warpgroups work on their
 // own slices or units, so one's unpacking covers the others' MMA and TMEM round trips.  Codes come by
 // TMA, a ring of three slices per warpgroup.
 #pragma once
@@ -119,7 +119,7 @@ w4_wide_kernel(const __grid_constant__ CUtensorMap codes, const W4Args a) {
     tmem_alloc(smem_u32(&tmem_slot), 512);
     tmem_relinquish();
   }
-  if (a.first) wait_dependency();
+  if (a.first) wait_dependency();  // else the call's first kernel has, before this one could start (W4Args::first)
   const int outs = MODE == kGateUp ? a.N / 2 : a.N;
   const int blocks = (outs + kOut - 1) / kOut;
   const int slices = (a.K + kSliceK - 1) / kSliceK;
@@ -141,7 +141,7 @@ w4_wide_kernel(const __grid_constant__ CUtensorMap codes, const W4Args a) {
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  launch_dependents();  // what follows allocates TMEM after this
+  launch_dependents();  // behind the wait above, and what follows allocates TMEM after this: as in w4_narrow.cuh
   const uint32_t tmem = tmem_slot;
   if (total == 0) {
     wait_dependency();  // what follows may rely on the kernel before this one
