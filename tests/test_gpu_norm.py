@@ -310,3 +310,24 @@ def test_codes_feed_a_dense_w8a8_expert():
         assert rel_max_err(f64(Y), ref) <= FP8_TOL
     finally:
         L.close()
+
+
+@pytest.mark.parametrize("H", [16384, 16385])
+def test_outputs_past_32_bits(H):
+    """More than 2^31 elements in the rows that are read and written, on 16-byte boundaries and off them."""
+    T = (1 << 31) // H + 200
+    x = torch.empty((T, H), dtype=BF16, device="cuda")
+    out, codes = torch.empty_like(x), torch.empty((T, H), dtype=torch.float8_e4m3fn, device="cuda")
+    scale = torch.empty((T,), device="cuda")
+    g = torch.ones((H,), device="cuda")
+    gen = torch.Generator().manual_seed(H)
+    rows = [0, 1, (1 << 31) // H - 1, (1 << 31) // H, (1 << 31) // H + 1, T - 1]
+    x.zero_()
+    for r in rows:
+        x[r] = torch.randn((H,), generator=gen).to(BF16)
+    call(x, None, g, None, out, codes, scale)
+    torch.cuda.synchronize()
+    check(x[rows], None, g, None, out[rows], codes[rows], scale[rows])
+    empty = torch.ones((T,), dtype=torch.bool)
+    empty[rows] = False
+    assert (scale.cpu()[empty] == 1).all() and float(out[2:100].abs().max()) == 0

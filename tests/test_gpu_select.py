@@ -367,3 +367,42 @@ def test_a_service_serves_under_the_routing_that_was_set():
         assert torch.equal(got[1], L.forward(T=7).cpu())
     finally:
         L.close()
+
+
+def test_stage_events_around_a_routing():
+    """Timing events between the stages, the router's two among them: the same output, and times in order."""
+    cfg = synth.MoEConfig("routed", T=64, H=256, E=16, k=2, I=128, S=1, seed=46)
+    L = Layer(cfg, redraws={})
+    try:
+        L.mod.set_routing(routing(GROUPED), torch.linspace(0.2, -0.2, 16, device="cuda"))
+        want = L.forward()
+        events = [torch.cuda.Event(enable_timing=True) for _ in range(afd.AFD_FFN_NUM_STAGES + 1)]
+        for e in events:
+            e.record()                                   # so that they exist
+        torch.cuda.synchronize()
+        L.mod.set_stage_events(events)
+        got = [L.forward() for _ in range(3)]
+        torch.cuda.synchronize()
+        L.mod.set_stage_events([])
+        assert all(torch.equal(g, want) for g in got)
+        assert all(a.elapsed_time(b) >= 0 for a, b in zip(events, events[1:]))
+    finally:
+        L.close()
+
+
+def test_tokens_past_32_bits():
+    """More than 2^31 logits and more than 2^31 / 4 results."""
+    E, k = 8, 2
+    T = (1 << 28) + 77
+    logits = torch.zeros((T, E), dtype=torch.bfloat16, device="cuda")
+    at = [0, (1 << 28) - 1, 1 << 28, T - 1]
+    some = torch.randn((len(at), E), generator=torch.Generator().manual_seed(13)).to(torch.bfloat16)
+    logits[at] = some.cuda()
+    idx = torch.full((T, k), 99, dtype=torch.int32, device="cuda")
+    w = torch.full((T, k), 99.0, device="cuda")
+    assert afd.afd_ffn_select_experts(logits, None, T, E, k, routing(PLAIN), idx, w) == afd.AFD_OK
+    torch.cuda.synchronize()
+    ri, rw = op.select_experts(some.double().numpy(), None, k, **PLAIN)
+    assert np.array_equal(idx[at].cpu().numpy(), ri)
+    assert (np.abs(w[at].double().cpu().numpy() - rw) <= 64 * U * rw).all()
+    assert (idx[1: 1000] == torch.tensor([0, 1], device="cuda")).all() and int(idx.max()) < E and float(w.max()) <= 1

@@ -650,3 +650,95 @@ def test_tokens_with_no_expert_left(T):
     ref = (rw[:, :, None] * yr).sum(1)
     tol = (rw[:, :, None] * (tr + (64 + k + 1) * U * np.abs(yr))).sum(1) * (1 + 2.0 ** -8) + 2.0 ** -8 * np.abs(ref)
     assert (np.abs(f64(out) - ref) <= tol).all() and (out[0] == 0).all()
+
+
+# ------------------------------------------------------------------ the ends of the ranges
+def test_rows_and_results_past_32_bits():
+    """The most rows that are taken, with more than 2^31 inputs and more than 2^31 results."""
+    gen = torch.Generator().manual_seed(40)
+    n, K, N, E = 1 << 22, 544, 520, 3
+    w = W4(gen, E, N, K, 32, True, F32)
+    counts = [n - 70, 0, 65]
+    x = torch.zeros((n, K), dtype=BF16, device="cuda")
+    at = [0, 63, 64, (1 << 31) // K, (1 << 31) // K + 1, (1 << 31) // N, n - 71, n - 70, n - 6]
+    some = rows_of(gen, len(at), K)
+    x[at] = some.cuda()
+    y = torch.full((n, N), 7.0, device="cuda")
+    c = torch.tensor(counts, dtype=torch.int32, device="cuda")
+    assert afd.afd_ffn_w4_rows(w.plan, E, x, c, n, y) == afd.AFD_OK
+    torch.cuda.synchronize()
+    ref, a = op.w4_rows(f64(some), w, [7, 0, 2])
+    assert (np.abs(f64(y[at]) - ref) <= rows_tol(a, ref, K, F32)).all()
+    assert (y[n - 5:] == 7.0).all() and (y[(1 << 31) // N + 1: n - 71] == 0).all()
+    assert afd.afd_ffn_rows_error() == afd.AFD_OK
+
+
+def test_scratch_past_32_bits():
+    """SwiGLU rows with more than 2^31 terms between the two products."""
+    gen = torch.Generator().manual_seed(41)
+    n, H, I = (1 << 21) + 33, 64, 544
+    w13, w2 = W4(gen, 1, 2 * I, H, 32), W4(gen, 1, H, I, 32, True)
+    x = torch.zeros((n, H), dtype=BF16, device="cuda")
+    at = [0, (1 << 31) // (2 * I) - 1, (1 << 31) // (2 * I), (1 << 31) // (2 * I) + 1, n - 1]
+    some = rows_of(gen, len(at), H)
+    x[at] = some.cuda()
+    y = torch.full((n, H), 7.0, device="cuda")
+    scratch = torch.empty((afd.afd_ffn_w4_scratch_bytes(n, I),), dtype=torch.uint8, device="cuda")
+    assert afd.afd_ffn_w4_expert_rows(w13.plan, w2.plan, 1, x, None, n, y, scratch) == afd.AFD_OK
+    torch.cuda.synchronize()
+    ref = op.w4_expert_rows(f64(some), w13, w2, [len(at)])
+    assert (np.abs(f64(y[at]) - ref) <= experts_tol(f64(some), w13, w2, [len(at)], ref, H, I, F32)).all()
+    assert (y[1:1000] == 0).all()
+
+
+def test_captured_behind_a_fork_and_a_join():
+    """A graph in which the norm and the selection run on streams of their own and the experts wait for both:
+    kernels that may start early behind more than one other."""
+    gen = torch.Generator().manual_seed(42)
+    T, H, I, E, k = 24, 512, 256, 8, 2
+    x = torch.randn((T, H), generator=gen).to(BF16).cuda()
+    logits = torch.randn((T, E), generator=gen).cuda()
+    gamma = torch.ones((H,), device="cuda")
+    w13, w2 = W4(gen, E, 2 * I, H, 128, True), W4(gen, E, H, I, 64)
+    cfg = afd.afd_ffn_norm_cfg(T=T, H=H, residual_dtype=afd.AFD_DT_BF16, gamma_dtype=afd.AFD_DT_F32, eps=1e-6)
+    route = afd.afd_ffn_routing(score=1, n_groups=1, topk_groups=1, group_best=1, renormalise=1, weight_scale=1.0)
+    i32 = lambda *s: torch.zeros(s, dtype=torch.int32, device="cuda")                  # noqa: E731
+    hidden, out = torch.zeros_like(x), torch.zeros_like(x)
+    idx, w, counts, offsets, pos, src = i32(T, k), torch.zeros((T, k), device="cuda"), i32(E), i32(E + 1), i32(T, k), i32(T * k)
+    rows, Y = torch.zeros((T * k, H), dtype=BF16, device="cuda"), torch.zeros((T * k, H), device="cuda")
+    scratch_d = i32(2 * E)
+    scratch_w = torch.zeros((afd.afd_ffn_w4_scratch_bytes(T * k, I),), dtype=torch.uint8, device="cuda")
+    dense, scratch_s = torch.zeros((T, H), device="cuda"), torch.zeros((afd.afd_ffn_w4_scratch_bytes(T, I),), dtype=torch.uint8, device="cuda")
+    ok = afd.AFD_OK
+
+    def layer(main, side):
+        side.wait_stream(main)
+        assert afd.afd_ffn_select_experts(logits, None, T, E, k, route, idx, w, stream=side) == ok
+        assert afd.afd_ffn_add_rmsnorm(cfg, x, None, gamma, None, hidden, stream=main) == ok
+        main.wait_stream(side)
+        assert afd.afd_ffn_add_rmsnorm(cfg, hidden, None, gamma, None, hidden, stream=main) == ok      # behind both
+        side.wait_stream(main)
+        one = afd.afd_ffn_w4(w13.plan.codes, w13.plan.scale, w13.plan.zero, 2 * I, H, 128, afd.AFD_DT_BF16)
+        two = afd.afd_ffn_w4(w2.plan.codes, w2.plan.scale, w2.plan.zero, H, I, 64, afd.AFD_DT_BF16)
+        assert afd.afd_ffn_w4_expert_rows(one, two, 1, hidden, None, T, dense, scratch_s, stream=side) == ok
+        assert afd.afd_ffn_dispatch_rows(hidden, idx, T, k, E, H, counts, offsets, pos, src, rows, scratch_d, stream=main) == ok
+        assert afd.afd_ffn_w4_expert_rows(w13.plan, w2.plan, E, rows, counts, T * k, Y, scratch_w, stream=main) == ok
+        main.wait_stream(side)
+        assert afd.afd_ffn_combine_rows(Y, dense, w, pos, T, k, H, out, stream=main) == ok
+
+    main, side = torch.cuda.Stream(), torch.cuda.Stream()
+    main.wait_stream(torch.cuda.current_stream())
+    layer(main, side)
+    torch.cuda.synchronize()
+    want, wi = out.clone(), idx.clone()
+    assert torch.isfinite(want).all() and want.abs().max() > 0
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=main):
+        layer(main, side)
+    for t in (hidden, out, idx, w, rows, Y, dense):
+        t.zero_()
+    for _ in range(5):
+        graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(out, want) and torch.equal(idx, wi)
+    assert afd.afd_ffn_rows_error() == ok
