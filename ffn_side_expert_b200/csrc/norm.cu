@@ -378,16 +378,17 @@ void launch_norm(const NormArgs& a, int T, cudaStream_t s) {
   }
 }
 
-// Shifted pieces against single elements: 4000 rows of 7001 (fp32 residual, both outputs) 86 us and 151 us,
-// 515 rows of 4097 8.2 and 9.1, 3000 rows of 2345 20 and 29; 8000 rows of 301 13.5 and 10.8.  Four rows on
-// an SM rather than two: 86 against 107 us.
+// Shifted pieces against single elements: 4000 rows of 7001 (fp32 residual, both outputs) 88 us and 150 us,
+// 515 rows of 4097 8.7 and 10.4, 3000 rows of 2345 22 and 29; 8000 rows of 301 13.5 and 10.8.  Four rows on
+// an SM rather than two: 88 against 107 us.
 constexpr int kShiftedMinH = 512;
 
 template <typename RT, typename GT>
 void launch_shifted(const NormArgs& a, int T, cudaStream_t s) {
   const int pieces = (a.H + 14) / 8;  // at most
-  // At most 32 elements a thread, as in the other forms: a row of more than 4096 pieces is a thread's fifth one
-  // only where its first and last are parts.
+  // At most 32 elements a thread, as in the other forms, so that a row's sum of squares is as exact: a thread has a
+  // fifth piece only in rows of more than 4096 pieces, whose first and last are parts.  Five whole ones took 210 us
+  // for 2000 rows of 24001, four take 198; 4000 rows of 9001 126 and 130.
   const int per = pieces <= 256 ? 1 : pieces <= 1024 ? 2 : 4, threads = std::min(1024, (pieces + per * 32 - 1) / (per * 32) * 32);
   if (per == 1) launch_dependent(add_rmsnorm_shifted_kernel<1, 256, 4, RT, GT>, T, threads, 0, s, a);
   else if (per == 2) launch_dependent(add_rmsnorm_shifted_kernel<2, 512, 4, RT, GT>, T, threads, 0, s, a);

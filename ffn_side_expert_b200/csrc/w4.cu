@@ -16,8 +16,8 @@
 // unpacking with more instructions around it (one token's eight experts of H = 7168, I = 2048: 66 us
 // against 60; 128 rows on 64 experts of 4096 x 1024: 143 against 101).
 //
-// What bounds it.  At the HBM rate an SM gets 46 codes a clock, and its integer pipe does 64 lane
-// operations; so the unpacking decides.  A word of eight codes takes nine instructions, five of
+// At the HBM rate an SM gets 46 codes a clock, and its integer pipe does 64 lane operations; so the unpacking
+// has to be short (what bounds each kernel stands there).  A word of eight codes takes nine instructions, five of
 // them integer: one shift, four masks and four bf16x2 FMAs that take the zero point off
 // (unpack_word).
 #include <cuda_bf16.h>

@@ -7,10 +7,13 @@
 // columns of each slice, and a lane reads those of its own slice: what a wider MMA computes beside them
 // costs nothing, and units of fewer rows spread few experts over the SMs.
 //
-// What bounds it: instructions.  At the HBM rate an SM gets 46 codes a clock, and unpacking alone takes 1.1
-// instructions a code; what a step takes besides (waits, barrier, scales, MMA issue, accumulators) is as
-// much again for 128 inputs, which is why a step takes 256 where TMEM has room.  The
-// accumulators of a step are read only when the next step's codes are there, so the MMAs run meanwhile.
+// What bounds it: the chain of a step, at the 12 or 16 warps an SM that TMEM leaves room for, and whole units in
+// rounds (one token's eight experts of H = 7168, I = 2048: 20 and 12 steps, where 16.1 and 8.1 would do if all
+// groups got the same; 59 us for 28 of bytes).  At the HBM rate an SM gets 46 codes a clock, and unpacking
+// alone takes 1.1 instructions a code; what a step takes besides (waits, barrier, scales, MMA issue,
+// accumulators) is as much again for 128 inputs, which is why a step takes 256 where TMEM has room.  Issue
+// is at half.  The accumulators of a step are read only when the next step's codes are there, so the MMAs
+// run meanwhile.
 #pragma once
 
 namespace afd {
