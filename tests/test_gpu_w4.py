@@ -523,7 +523,7 @@ def test_calls_that_nothing_waits_between(captured):
     norm and the counts from a copy just before, other rows and counts of another call follow at once, and what
     the call read and its scratch are overwritten behind it.  Each call's results are those of a call alone."""
     gen = torch.Generator().manual_seed(14)
-    E, H, I, rounds = 6, 2048, 1536, 12
+    E, H, I, rounds = 6, 2048, 1600, 12
     w13, w2 = W4(gen, E, 2 * I, H, 128, True), W4(gen, E, H, I, 64)
     lots = [[70, 3, 0, 20, 1, 9], [1, 0, 40, 2, 60, 0], [0, 103, 0, 0, 0, 0]]
     n = 103
